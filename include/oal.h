@@ -25,8 +25,8 @@
  *    default stream).  A return of OAL_OK means the work was validated and enqueued.
  *  - Return value: OAL_OK (0) or a negative oal_status.  Nothing aborts or throws.  Argument
  *    errors are found on the host before anything is enqueued.  Errors that only the device
- *    can see (a group id outside 1..G[h], G[h] outside 1..OAL_G_MAX, a bounded wait that ran
- *    out) set a device-side error word instead; read and clear it with oal_device_error().
+ *    can see (a group id outside 1..G[h], G[h] outside 1..OAL_G_MAX, a decay, length or parent
+ *    index out of range, a bounded wait that ran out) set a device-side error word instead; read and clear it with oal_device_error().
  *  - Layouts: q [B][Hq][T][dh], k [B][Hkv][T][dh], v [B][Hkv][T][dv] in the element type of
  *    oal_shape.dtype; out [B][Hq][T][dv] fp32.  Query head h reads key/value head
  *    floor(h * Hkv / Hq) (grouped-query attention; Hq must be a multiple of Hkv).
@@ -67,7 +67,9 @@ typedef enum {
     OAL_ERR_CUDA = -6,        /* a CUDA launch or runtime call failed */
     OAL_ERR_TIMEOUT = -7,     /* device: a bounded wait gave up */
     OAL_ERR_WORKSPACE = -8,   /* workspace NULL or smaller than the query function says */
-    OAL_ERR_STATE = -9        /* state buffer does not match the shape */
+    OAL_ERR_STATE = -9,       /* state buffer does not match the shape */
+    OAL_ERR_VALUE = -10,      /* device: a decay, length or parent out of range (clamped) */
+    OAL_ERR_OVERLAP = -11     /* source and destination overlap */
 } oal_status;
 
 /* Problem description shared by every call.  Size limits checked on the host (OAL_ERR_SHAPE):
@@ -380,6 +382,117 @@ int oal_backward(const void* q, const void* k, const void* v, const int32_t* gro
  * n_parts = 0 writes zeros.  Device pointers, 16-byte aligned; n a multiple of 4 when
  * n_parts > 0.  `out` must not overlap `parts`. */
 int oal_state_prefix_sum(const float* parts, int n_parts, size_t n, float* out, void* stream);
+
+/* ---- linear attention with a decay per key/value head --------------------------------------
+ *
+ *     S_t = l S_{t-1} + k_t v_t^T,   o_t = scale S_t^T q_t,   l = exp(log_decay[kv head])
+ *
+ * that is o_i = scale sum_{j<=i} l^(i-j) (q_i . k_j) v_j: attention without a normaliser whose
+ * weights fade with distance, as the layers of a model that keep a short state instead of the
+ * quadratic one above.  Same layouts, sizes and conventions (q [B][Hq][T][64], k and v
+ * [B][Hkv][T][64], Hq / Hkv <= 8, contiguous, 16-byte aligned) with these differences:
+ *  - the outputs and gradients have the element type of the inputs (oal_shape.dtype);
+ *  - log_decay [Hkv] fp32 on the device, each at most 0 (0: no decay; -inf: a token sees only
+ *    itself).  A constant of the layer: it gets no gradient.  A positive or NaN entry sets
+ *    OAL_ERR_VALUE in the device error word and counts as 0;
+ *  - the state is [B][Hkv][64][64] fp32 (row = key dimension, column = value dimension) with no
+ *    header; zeros are an empty sequence;
+ *  - lens [B] int32 on the device, or NULL: the tokens of each sequence of a padded batch,
+ *    0 <= lens[b] <= T.  What lies behind them in q, k, v (and dout) is not used, whatever it
+ *    holds, and the rows behind them of out (and of the gradients) are left as they were.  An
+ *    entry out of range sets OAL_ERR_VALUE and is clamped;
+ *  - oal_shape.chunk is not used.
+ * Within a sequence, a token that holds an infinity or a NaN may reach every row of its chunk of
+ * 128 tokens, earlier rows included, and every later row.  bf16 inputs are multiplied on tensor
+ * cores (bf16 operands, fp32 accumulation and fp32 states); fp32 inputs in fp32 on CUDA cores.
+ * Every sum has a fixed order, so results are bit-reproducible. */
+
+/* Bytes of a state for `s` (B, Hkv used). */
+int oal_decay_state_bytes(const oal_shape* s, size_t* bytes);
+
+/* Scratch of oal_decay_prefill and oal_decay_prefill_continue for `s`.  Its contents need no
+ * initialisation and mean nothing after the call. */
+int oal_decay_prefill_workspace_bytes(const oal_shape* s, size_t* bytes);
+
+/* Prompts: out [B][Hq][T][64] for every token, and the state after the last.  out == NULL
+ * computes the state alone (q may be NULL), state == NULL the outputs alone.  B * T == 0 leaves
+ * zeros in the state.  B * Hq <= 65535. */
+int oal_decay_prefill(const void* q, const void* k, const void* v, const float* log_decay,
+                      float scale, const int32_t* lens, void* out, float* state, void* workspace,
+                      size_t workspace_bytes, const oal_shape* s, void* stream);
+
+/* The same from the state that `state` holds, which is replaced by the state after the last
+ * token (required; out may be NULL). */
+int oal_decay_prefill_continue(const void* q, const void* k, const void* v,
+                               const float* log_decay, float scale, const int32_t* lens,
+                               void* out, float* state, void* workspace, size_t workspace_bytes,
+                               const oal_shape* s, void* stream);
+
+/* One token for every sequence (T of `s` is not used): q [B][Hq][1][64], k, v [B][Hkv][1][64],
+ * out [B][Hq][1][64].  With src == NULL `state` is updated in place.  With src (src_B sequences)
+ * and parents [B] int32 on the device, sequence b goes on from sequence parents[b] of src, and
+ * `state` receives the result: a beam search's reordering and step in one pass.  src and state
+ * must not overlap (OAL_ERR_OVERLAP); the same parent may be named any number of times; one out
+ * of range sets OAL_ERR_VALUE and is clamped.  Memory-bound: the state is read and written once. */
+int oal_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
+                   float scale, const float* src, int src_B, const int32_t* parents, float* state,
+                   void* out, const oal_shape* s, void* stream);
+
+/* Scratch of oal_decay_backward for `s`. */
+int oal_decay_backward_workspace_bytes(const oal_shape* s, size_t* bytes);
+
+/* Gradients of oal_decay_prefill (state == NULL) or oal_decay_prefill_continue (`state`: the
+ * state it started from), given dout = dLoss/dout [B][Hq][T][64] and dlast = dLoss/d(state after
+ * the last token) [B][Hkv][64][64] fp32 or NULL for zero:
+ *     dq [B][Hq][T][64], dk and dv [B][Hkv][T][64] (summed over the query heads of a key/value
+ *     head), dstate [B][Hkv][64][64] fp32 = dLoss/d(state before the first token), or NULL.
+ * dstate may be dlast.  The states are recomputed; nothing of the forward pass has to be kept. */
+int oal_decay_backward(const void* q, const void* k, const void* v, const float* log_decay,
+                       float scale, const int32_t* lens, const void* dout, const float* state,
+                       const float* dlast, void* dq, void* dk, void* dv, float* dstate,
+                       void* workspace, size_t workspace_bytes, const oal_shape* s, void* stream);
+
+/* ---- beam search on recurrent state ------------------------------------------------------- */
+
+/* Scratch of oal_beam_select. */
+int oal_beam_select_workspace_bytes(int B, int beams, int V, int n, int dtype, size_t* bytes);
+
+/* The n best continuations of each of B searches over its `beams` rows and V tokens: a candidate
+ * (row r, token t) scores running[r] + log_softmax(logits[r])[t].
+ *   logits [B * beams] rows of V values (dtype: oal_dtype), row_stride >= V elements apart, the
+ *   first 16-byte aligned; running [B * beams] fp32; ended [B * beams] bytes, or NULL;
+ *   scores [B][n] fp32, parents [B][n] int32 (rows of the B * beams, as oal_state_reorder and the
+ *   beam steps take them), tokens [B][n] int32, best first.
+ * Equal scores come in the order of (row, token).  An ended row (ended[r] != 0) goes on with
+ * pad_token alone, at its running score, and its logits are not read.  A candidate that cannot
+ * be (a logit of -inf; a row with a NaN or +inf logit, with no finite logit, or whose running
+ * score is not finite; another token of an ended row) scores -inf, and is returned where no
+ * others are left.  Scores are formed in 64 bits and rounded once.
+ * n <= 32, n <= beams * V, beams <= 256, beams * V < 2^31 - 64, B * beams <= 65535. */
+int oal_beam_select(const void* logits, long long row_stride, int dtype, const float* running,
+                    const uint8_t* ended, int pad_token, int B, int beams, int V, int n,
+                    float* scores, int32_t* parents, int32_t* tokens, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* Copies prefix states: sequence b of `dst` (a state buffer of `s`) becomes sequence parents[b]
+ * of `src` (a state buffer of src_B sequences, the same Hq and Hkv).  Header and coefficient
+ * tables are copied too, so dst needs no initialisation, and s->B may differ from src_B (a
+ * prompt's state spread over its beams).  parents [B] int32 on the device; the same parent may
+ * be named any number of times; one out of range sets OAL_ERR_VALUE and is clamped.  src and
+ * dst must not overlap (OAL_ERR_OVERLAP). */
+int oal_state_reorder(const void* src, int src_B, const int32_t* parents, void* dst,
+                      const oal_shape* s, void* stream);
+
+/* The same for the states of decayed linear attention ([B][Hkv][64][64] fp32). */
+int oal_decay_state_reorder(const float* src, int src_B, const int32_t* parents, float* dst,
+                            const oal_shape* s, void* stream);
+
+/* oal_decode_step of sequence b from sequence parents[b] of `src`, into `dst`: the result of
+ * oal_state_reorder followed by oal_decode_step, bit for bit, in one pass over the states
+ * instead of two.  Arguments as for those two; src is left as it was. */
+int oal_decode_step_beam(const void* q, const void* k, const void* v, const void* src, int src_B,
+                         const int32_t* parents, void* dst, float* out, void* workspace,
+                         size_t workspace_bytes, const oal_shape* s, void* stream);
 
 /* Reads the device-side error word (OAL_OK or a negative oal_status set by a kernel since
  * the last read), synchronising `stream`, and clears it. */

@@ -13,6 +13,13 @@ namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether the na bytes at a and the nb bytes at b share any.
+bool overlap(const void* a, size_t na, const void* b, size_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+
 // q, k, v, out: required and aligned only when there is at least one token to process.
 int check_io(const oal_shape* s, const void* q, const void* k, const void* v, const void* out)
 {
@@ -96,6 +103,8 @@ const char* oal_status_string(int status)
     case OAL_ERR_CUDA: return "CUDA launch or runtime error";
     case OAL_ERR_TIMEOUT: return "a bounded device wait gave up";
     case OAL_ERR_WORKSPACE: return "workspace missing or too small";
+    case OAL_ERR_VALUE: return "a decay, length or parent index out of range (clamped on device)";
+    case OAL_ERR_OVERLAP: return "source and destination overlap";
     case OAL_ERR_STATE: return "state buffer does not match the shape";
     default: return "unknown status";
     }

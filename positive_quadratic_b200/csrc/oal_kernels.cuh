@@ -24,7 +24,8 @@ int decode_slabs();
 
 int launch_decode(const void* q, const void* k, const void* v, void* state, float* out,
                   float* part, int B, int Hq, int Hkv, int dtype,
-                  cudaStream_t st);
+                  cudaStream_t st, const void* src = nullptr, int src_B = 0,
+                  const int32_t* parents = nullptr);
 
 // ungrouped Hadamard form (oal_hadamard.cu): prefill on CUDA cores, or the dense O(T^2) form
 int launch_hadamard(const void* q, const void* k, const void* v, const float* a, const float* b,

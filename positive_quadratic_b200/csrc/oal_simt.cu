@@ -469,24 +469,45 @@ constexpr int kDecThreads = 256;
 constexpr int kDecBatch = 2;   // rows per thread per batch (a half warp per row); the next batch is in flight
 constexpr int kDecWarps = kDecThreads / 32;
 
-template <typename Tin, int kGrp>  // kGrp = Hq / Hkv query heads per kv head
+// kBeam: sequence b continues the state of sequence parents[b] of `src` (a beam search's
+// reordering), and the whole result (sums, padding rows, coefficients) goes to `state`, which
+// holds nothing before.  The sums are read and written once either way, so the reordering by
+// itself, another read and write of them, is saved; several beams of one parent read it from L2
+// (the loads are not marked for eviction).
+template <typename Tin, int kGrp, bool kBeam>  // kGrp = Hq / Hkv query heads per kv head
 __global__ void __launch_bounds__(kDecThreads, 4) decode_kernel(const Tin* __restrict__ q,
                                                               const Tin* __restrict__ k,
                                                               const Tin* __restrict__ v,
                                                               unsigned char* __restrict__ state,
                                                               float* __restrict__ out,
                                                               float* __restrict__ part,
-                                                              int Hq, int Hkv)
+                                                              int Hq, int Hkv,
+                                                              const unsigned char* __restrict__ src,
+                                                              int src_B,
+                                                              const int32_t* __restrict__ parents)
 {
     const int slab = blockIdx.x, bkv = blockIdx.y, nslab = gridDim.x;
     constexpr int grp = kGrp;
     const int b = bkv / Hkv, kv = bkv % Hkv, h0 = kv * grp;
     const int tid = threadIdx.x, lane4 = tid & 15, rsub = tid >> 4, warp = tid >> 5;
-    const float* coef = reinterpret_cast<const float*>(state + kHeaderBytes);
+    const float* coef = reinterpret_cast<const float*>((kBeam ? src : state) + kHeaderBytes);
     float* unit = reinterpret_cast<float*>(state + kHeaderBytes + coef_bytes(Hq)) +
                   size_t(bkv) * kFP * kW;
     float* Hv = unit;
     float* z = unit + size_t(kFP) * kDV;
+    const float* unit_in = unit;
+    if constexpr (kBeam) {
+        int from = parents[b];
+        if (from < 0 || from >= src_B) {
+            if (tid == 0) raise_error(OAL_ERR_VALUE);
+            from = from < 0 ? 0 : src_B - 1;
+        }
+        unit_in = reinterpret_cast<const float*>(src + kHeaderBytes + coef_bytes(Hq)) +
+                  (size_t(from) * Hkv + kv) * kFP * kW;
+    }
+    const float* Hv_in = unit_in;
+    const float* z_in = unit_in + size_t(kFP) * kDV;
+    auto load4 = [](const float4* p) { return kBeam ? __ldg(p) : __ldcs(p); };
 
     __shared__ __align__(16) float vh[kW + 3];
     __shared__ float kh[kDA];
@@ -506,7 +527,7 @@ __global__ void __launch_bounds__(kDecThreads, 4) decode_kernel(const Tin* __res
     for (int x = 0; x < kDecBatch; ++x) {
         const int row = rsub + kRowStep * x;
         if (row < nrows)
-            hv[x] = __ldcs(reinterpret_cast<const float4*>(Hv + size_t(f0 + row) * kDV) + lane4);
+            hv[x] = load4(reinterpret_cast<const float4*>(Hv_in + size_t(f0 + row) * kDV) + lane4);
     }
 
     // this thread's row of the slab (kDecRows < kDecThreads: at most one): its readout
@@ -519,7 +540,26 @@ __global__ void __launch_bounds__(kDecThreads, 4) decode_kernel(const Tin* __res
     if (has_row) {
 #pragma unroll
         for (int g = 0; g < kGrp; ++g) cpre[g] = coef[size_t(h0 + g) * kFP + f0 + tid];
-        zpre = z[f0 + tid];
+        zpre = z_in[f0 + tid];
+    }
+    if constexpr (kBeam) {
+        // what the step itself does not write: the coefficients (by sequence 0's blocks), and
+        // the padding rows (by the last slab's)
+        float* coef_out = reinterpret_cast<float*>(state + kHeaderBytes);
+        const bool last = slab == nslab - 1;
+        if (b == 0) {
+#pragma unroll
+            for (int g = 0; g < kGrp; ++g) {
+                if (has_row) coef_out[size_t(h0 + g) * kFP + f0 + tid] = cpre[g];
+                if (last && tid < kFP - kF)
+                    coef_out[size_t(h0 + g) * kFP + kF + tid] = coef[size_t(h0 + g) * kFP + kF + tid];
+            }
+        }
+        if (last) {
+            for (int e = tid; e < (kFP - kF) * kDV; e += kDecThreads)
+                Hv[size_t(kF) * kDV + e] = Hv_in[size_t(kF) * kDV + e];
+            if (tid < kFP - kF) z[kF + tid] = z_in[kF + tid];
+        }
     }
     if (tid < kD) {
         kh[tid] = to_f32(k[size_t(bkv) * kD + tid]);
@@ -561,7 +601,7 @@ __global__ void __launch_bounds__(kDecThreads, 4) decode_kernel(const Tin* __res
         for (int x = 0; x < kDecBatch; ++x) {
             const int row = base + kRowStep * (kDecBatch + x);
             if (row < nrows)
-                nx[x] = __ldcs(reinterpret_cast<const float4*>(Hv + size_t(f0 + row) * kDV) + lane4);
+                nx[x] = load4(reinterpret_cast<const float4*>(Hv_in + size_t(f0 + row) * kDV) + lane4);
         }
 #pragma unroll
         for (int x = 0; x < kDecBatch; ++x) {
@@ -641,7 +681,8 @@ template <int kGrp>
 __global__ void __launch_bounds__(256) decode_finish_kernel(const float* __restrict__ part,
                                                             float* __restrict__ out,
                                                             unsigned char* __restrict__ state,
-                                                            int Hq, int Hkv, int nslab)
+                                                            int Hq, int Hkv, int nslab,
+                                                            const unsigned char* __restrict__ src)
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // the partials are complete
     constexpr int grp = kGrp;
@@ -666,7 +707,13 @@ __global__ void __launch_bounds__(256) decode_finish_kernel(const float* __restr
         const int g = e / kDV, n = e % kDV;
         out[(size_t(b) * Hq + h0 + g) * kDV + n] = ufin[g][n] / ufin[g][kDV];
     }
-    if (threadIdx.x == 0 && bkv == 0) reinterpret_cast<StateHeader*>(state)->tokens += 1;
+    if (threadIdx.x != 0 || bkv != 0) return;
+    StateHeader* hd = reinterpret_cast<StateHeader*>(state);
+    if (src) {  // a step into another buffer: its header, with that buffer's batch size
+        *hd = *reinterpret_cast<const StateHeader*>(src);
+        hd->B = gridDim.x / Hkv;
+    }
+    hd->tokens += 1;
 }
 
 int launch_prep(const int32_t* gid, const float* L, const int32_t* G, float eps, void* state,
@@ -907,7 +954,8 @@ int launch_dense(const void* q, const void* k, const void* v, const int32_t* gid
 int decode_slabs() { return (kF + kDecRows - 1) / kDecRows; }
 
 int launch_decode(const void* q, const void* k, const void* v, void* state, float* out,
-                  float* part, int B, int Hq, int Hkv, int dtype, cudaStream_t st)
+                  float* part, int B, int Hq, int Hkv, int dtype, cudaStream_t st,
+                  const void* src, int src_B, const int32_t* parents)
 {
     if (B == 0) return OAL_OK;
     const dim3 grid(decode_slabs(), B * Hkv);
@@ -918,14 +966,15 @@ int launch_decode(const void* q, const void* k, const void* v, void* state, floa
         constexpr int g = decltype(G)::value;
         {
             LaunchScope ls("decode", st);
-            if (bf)
-                decode_kernel<__nv_bfloat16, g><<<grid, kDecThreads, 0, st>>>(
-                    static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-                    static_cast<const __nv_bfloat16*>(v), s, out, part, Hq, Hkv);
-            else
-                decode_kernel<float, g><<<grid, kDecThreads, 0, st>>>(
-                    static_cast<const float*>(q), static_cast<const float*>(k),
-                    static_cast<const float*>(v), s, out, part, Hq, Hkv);
+            const auto* from = static_cast<const unsigned char*>(src);
+            auto run = [&](auto t, auto beam) {
+                using T = decltype(t);
+                decode_kernel<T, g, decltype(beam)::value><<<grid, kDecThreads, 0, st>>>(
+                    static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v), s,
+                    out, part, Hq, Hkv, from, src_B, parents);
+            };
+            if (bf) src ? run(__nv_bfloat16{}, std::true_type{}) : run(__nv_bfloat16{}, std::false_type{});
+            else src ? run(float{}, std::true_type{}) : run(float{}, std::false_type{});
             const cudaError_t e = cudaGetLastError();
             if (e != cudaSuccess) return e;
         }
@@ -940,7 +989,8 @@ int launch_decode(const void* q, const void* k, const void* v, void* state, floa
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         return cudaLaunchKernelEx(&cfg, decode_finish_kernel<g>, static_cast<const float*>(part),
-                                  out, s, Hq, Hkv, int(grid.x));
+                                  out, s, Hq, Hkv, int(grid.x),
+                                  static_cast<const unsigned char*>(src));
     };
     cudaError_t e;
     switch (grp) {

@@ -24,7 +24,8 @@ G_MAX = 8
 FEATURES, FEATURES_PAD = 2145, 2176
 STATUS = {0: "OAL_OK", -1: "OAL_ERR_NULL", -2: "OAL_ERR_SHAPE", -3: "OAL_ERR_UNSUPPORTED",
           -4: "OAL_ERR_ALIGN", -5: "OAL_ERR_GROUPS", -6: "OAL_ERR_CUDA", -7: "OAL_ERR_TIMEOUT",
-          -8: "OAL_ERR_WORKSPACE", -9: "OAL_ERR_STATE"}
+          -8: "OAL_ERR_WORKSPACE", -9: "OAL_ERR_STATE", -10: "OAL_ERR_VALUE",
+          -11: "OAL_ERR_OVERLAP"}
 
 
 class Shape(ctypes.Structure):
@@ -113,6 +114,23 @@ def lib() -> ctypes.CDLL:
                          "oal_prefill_hadamard", "oal_dense_hadamard_gpu",
                          "oal_prefill_varlen_workspace_bytes", "oal_prefill_varlen"):
                 getattr(L, name).restype = ctypes.c_int
+            _I, _F = ctypes.c_int, ctypes.c_float
+            for name, args in {
+                    "oal_decay_state_bytes": [_PS, ctypes.POINTER(_SZ)],
+                    "oal_decay_prefill_workspace_bytes": [_PS, ctypes.POINTER(_SZ)],
+                    "oal_decay_prefill": [_VP] * 4 + [_F] + [_VP] * 4 + [_SZ, _PS, _VP],
+                    "oal_decay_prefill_continue": [_VP] * 4 + [_F] + [_VP] * 4 + [_SZ, _PS, _VP],
+                    "oal_decay_step": [_VP] * 4 + [_F, _VP, _I] + [_VP] * 3 + [_PS, _VP],
+                    "oal_decay_backward_workspace_bytes": [_PS, ctypes.POINTER(_SZ)],
+                    "oal_decay_backward": [_VP] * 4 + [_F] + [_VP] * 9 + [_SZ, _PS, _VP],
+                    "oal_beam_select_workspace_bytes": [_I] * 5 + [ctypes.POINTER(_SZ)],
+                    "oal_beam_select": [_VP, ctypes.c_longlong, _I, _VP, _VP] + [_I] * 5 +
+                                       [_VP] * 4 + [_SZ, _VP],
+                    "oal_state_reorder": [_VP, _I, _VP, _VP, _PS, _VP],
+                    "oal_decay_state_reorder": [_VP, _I, _VP, _VP, _PS, _VP],
+                    "oal_decode_step_beam": [_VP] * 4 + [_I] + [_VP] * 4 + [_SZ, _PS, _VP]}.items():
+                getattr(L, name).argtypes = args
+                getattr(L, name).restype = _I
             L.oal_profile_enable.argtypes = [ctypes.c_int]
             L.oal_profile_enable.restype = ctypes.c_int
             L.oal_profile_read.argtypes = [ctypes.POINTER(KernelStat), ctypes.c_int,
@@ -582,6 +600,301 @@ def backward_workspace(q, k, v) -> torch.Tensor:
     _check(lib().oal_backward_workspace_bytes(ctypes.byref(_shape_of(q, k, v, 64)),
                                               ctypes.byref(n)), "oal_backward_workspace_bytes")
     return empty_workspace(n.value, q.device)
+
+
+class _on:
+    """The device and stream of a call: tensors made inside belong to that stream, so that their
+    memory is not handed out again before the call's kernels are done with it.  Where the stream
+    is the device's current one already, nothing is switched."""
+
+    def __init__(self, device, stream):
+        self.ctx = []
+        if device.index is not None and device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for c in reversed(self.ctx):
+            c.__exit__(*exc)
+
+
+def _need(name, t, shape, dtype, device, optional=False):
+    """Refuses a tensor that is not a contiguous CUDA tensor of this shape, type and device."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is missing")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
+    return t.data_ptr()
+
+
+def _need_ws(ws, device):
+    if ws.device != device or not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _decay_args(q, k, v, log_decay, lens):
+    """(shape, the pointers of q, k, v, log_decay, lens) of a decayed linear attention call."""
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k, v must be [B, H, T, 64]")
+    B, Hq, T, d = q.shape
+    Hkv = k.shape[1]
+    shape = Shape(B, T, Hq, Hkv, d, v.shape[-1], 128, _dtype_code(q))
+    dev = q.device
+    kv = (B, Hkv, T, d)
+    return shape, (_need("q", q, q.shape, q.dtype, dev), _need("k", k, kv, q.dtype, dev),
+                   _need("v", v, kv, q.dtype, dev),
+                   _need("log_decay", log_decay, (Hkv,), torch.float32, dev),
+                   _need("lens", lens, (B,), torch.int32, dev, optional=True))
+
+
+def _bytes_of(query, shape) -> int:
+    n = _SZ(0)
+    _check(getattr(lib(), query)(ctypes.byref(shape), ctypes.byref(n)), query)
+    return n.value
+
+
+def decay_prefill_workspace(q, k, v) -> torch.Tensor:
+    """A workspace for decay_prefill and decay_prefill_continue on inputs of these shapes."""
+    shape = _shape_of(q, k, v, 128)
+    return empty_workspace(_bytes_of("oal_decay_prefill_workspace_bytes", shape), q.device)
+
+
+def decay_backward_workspace(q, k, v) -> torch.Tensor:
+    """A workspace for decay_backward on inputs of these shapes."""
+    shape = _shape_of(q, k, v, 128)
+    return empty_workspace(_bytes_of("oal_decay_backward_workspace_bytes", shape), q.device)
+
+
+def _decay_prefill(name, q, k, v, log_decay, scale, lens, out, state, want_out, workspace, stream,
+                   fresh):
+    shape, (pq, pk, pv, pg, pl) = _decay_args(q, k, v, log_decay, lens)
+    dev = q.device
+    with _on(dev, stream) as s:
+        if out is None and want_out:
+            # rows behind a sequence's end are not written
+            out = torch.empty_like(q) if lens is None else torch.zeros_like(q)
+        if state is None and fresh:
+            state = torch.empty(shape.B, shape.Hkv, 64, 64, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = empty_workspace(_bytes_of("oal_decay_prefill_workspace_bytes", shape), dev)
+        po = _need("out", out, q.shape, q.dtype, dev, optional=True) if want_out else None
+        ps = _need("state", state, (shape.B, shape.Hkv, 64, 64), torch.float32, dev)
+        pw, nw = _need_ws(workspace, dev)
+        _check(getattr(lib(), name)(pq, pk, pv, pg, scale, pl, po, ps, pw, nw,
+                                    ctypes.byref(shape), s), name)
+    return out, state
+
+
+def decay_prefill(q, k, v, log_decay, scale: float, lens=None, out=None, state=None,
+                  want_out: bool = True, workspace=None, stream=None):
+    """oal_decay_prefill: linear attention with decay exp(log_decay[kv head]) over prompts
+    q [B, Hq, T, 64], k and v [B, Hkv, T, 64] (bf16 or fp32), scores times `scale`; lens [B]
+    int32: the tokens of each sequence of a padded batch.  Returns (out like q, state
+    [B, Hkv, 64, 64] fp32); want_out=False computes the state alone (out is None)."""
+    return _decay_prefill("oal_decay_prefill", q, k, v, log_decay, scale, lens, out, state,
+                          want_out, workspace, stream, True)
+
+
+def decay_prefill_continue(q, k, v, log_decay, scale: float, state, lens=None, out=None,
+                           want_out: bool = True, workspace=None, stream=None):
+    """oal_decay_prefill_continue: the same from `state`, which is updated; returns out."""
+    return _decay_prefill("oal_decay_prefill_continue", q, k, v, log_decay, scale, lens, out,
+                          state, want_out, workspace, stream, False)[0]
+
+
+def decay_step(q, k, v, log_decay, scale: float, state, src=None, parents=None, out=None,
+               stream=None):
+    """oal_decay_step: one token, q [B, Hq, 1, 64], k and v [B, Hkv, 1, 64]; `state` is updated
+    in place, or with src [B', Hkv, 64, 64] and parents (int32, B of them) becomes the state of
+    the parents one token on.  Returns out like q."""
+    shape, (pq, pk, pv, pg, _) = _decay_args(q, k, v, log_decay, None)
+    if shape.T != 1:
+        raise ValueError("decay_step takes one token: q, k, v [B, H, 1, 64]")
+    dev = q.device
+    ps = _need("state", state, (shape.B, shape.Hkv, 64, 64), torch.float32, dev)
+    psrc = ppar = None
+    n = 0
+    if src is not None or parents is not None:
+        if src is None or parents is None:
+            raise ValueError("src and parents go together")
+        n = src.shape[0]
+        psrc = _need("src", src, (n, shape.Hkv, 64, 64), torch.float32, dev)
+        ppar = _parents(parents, shape.B, dev)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty_like(q)
+        _check(lib().oal_decay_step(pq, pk, pv, pg, scale, psrc, n, ppar, ps,
+                                    _need("out", out, q.shape, q.dtype, dev),
+                                    ctypes.byref(shape), s), "oal_decay_step")
+    return out
+
+
+def decay_backward(q, k, v, log_decay, scale: float, dout, lens=None, state=None, dlast=None,
+                   grads=None, dstate=None, workspace=None, stream=None) -> dict:
+    """oal_decay_backward: gradients of decay_prefill (state=None) or decay_prefill_continue
+    (`state`: the one it started from) for dout like q and dlast = dLoss/d(last state) or None.
+    `grads`: (dq, dk, dv) to write to.  Returns dict(dq, dk, dv, dstate)."""
+    shape, (pq, pk, pv, pg, pl) = _decay_args(q, k, v, log_decay, lens)
+    dev = q.device
+    st = (shape.B, shape.Hkv, 64, 64)
+    with _on(dev, stream) as s:
+        if grads is None:
+            # rows behind a sequence's end are not written
+            make = torch.empty_like if lens is None else torch.zeros_like
+            grads = make(q), make(k), make(v)
+        if dstate is None:
+            dstate = torch.empty(st, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = empty_workspace(_bytes_of("oal_decay_backward_workspace_bytes", shape), dev)
+        dq, dk, dv = grads
+        pw, nw = _need_ws(workspace, dev)
+        _check(lib().oal_decay_backward(
+            pq, pk, pv, pg, scale, pl, _need("dout", dout, q.shape, q.dtype, dev),
+            _need("state", state, st, torch.float32, dev, optional=True),
+            _need("dlast", dlast, st, torch.float32, dev, optional=True),
+            _need("dq", dq, q.shape, q.dtype, dev), _need("dk", dk, k.shape, q.dtype, dev),
+            _need("dv", dv, v.shape, q.dtype, dev),
+            _need("dstate", dstate, st, torch.float32, dev), pw, nw, ctypes.byref(shape), s),
+            "oal_decay_backward")
+    return dict(dq=dq, dk=dk, dv=dv, dstate=dstate)
+
+
+def _parents(parents, B, dev):
+    """Pointer of `parents`, int32, B of them in any shape ([B] or [searches, beams])."""
+    if parents.numel() != B:
+        raise ValueError(f"parents must hold {B} indices, got {parents.numel()}")
+    return _need("parents", parents, parents.shape, torch.int32, dev)
+
+
+def beam_select_workspace(B, beams, V, n, device, dtype=torch.float32) -> torch.Tensor:
+    """A workspace for beam_select of these sizes (either type of logits)."""
+    return empty_workspace(_select_bytes(B, beams, V, n, OAL_F32), device)
+
+
+def _select_bytes(B, beams, V, n, code) -> int:
+    nb = _SZ(0)
+    _check(lib().oal_beam_select_workspace_bytes(B, beams, V, n, code, ctypes.byref(nb)),
+           "oal_beam_select_workspace_bytes")
+    return nb.value
+
+
+def beam_select(logits, running, n: int, ended=None, pad_token: int = 0, scores=None,
+                parents=None, tokens=None, workspace=None, stream=None):
+    """oal_beam_select: of logits [B, beams, V] (bf16 or fp32; rows may lie further apart than V)
+    and running scores [B, beams] fp32, the n best candidates running + log_softmax of each
+    search; ended [B, beams] uint8 or bool marks rows that go on with pad_token alone.  Returns
+    (scores [B, n] fp32, parents [B, n] int32 rows of the B * beams, tokens [B, n] int32)."""
+    if logits.dim() != 3:
+        raise ValueError("logits must be [B, beams, V]")
+    B, beams, V = logits.shape
+    dev = logits.device
+    ld = logits.stride(1) if beams > 1 else (logits.stride(0) if B > 1 else V)
+    if not logits.is_cuda or (V > 1 and logits.stride(2) != 1) or ld < V or (
+            B > 1 and logits.stride(0) != beams * ld):
+        raise ValueError("logits must be a CUDA tensor whose rows are contiguous and equally "
+                         "spaced")
+    if ended is not None and ended.dtype is torch.bool:
+        ended = ended.view(torch.uint8)
+    code = _dtype_code(logits)
+    pr = _need("running", running, (B, beams), torch.float32, dev)
+    pe = _need("ended", ended, (B, beams), torch.uint8, dev, optional=True)
+    with _on(dev, stream) as s:
+        if scores is None:
+            scores = torch.empty(B, n, dtype=torch.float32, device=dev)
+        if parents is None:
+            parents = torch.empty(B, n, dtype=torch.int32, device=dev)
+        if tokens is None:
+            tokens = torch.empty(B, n, dtype=torch.int32, device=dev)
+        if workspace is None:
+            workspace = empty_workspace(_select_bytes(B, beams, V, n, code), dev)
+        pw, nw = _need_ws(workspace, dev)
+        _check(lib().oal_beam_select(
+            logits.data_ptr(), ld, code, pr, pe, pad_token, B, beams, V, n,
+            _need("scores", scores, (B, n), torch.float32, dev),
+            _need("parents", parents, (B, n), torch.int32, dev),
+            _need("tokens", tokens, (B, n), torch.int32, dev), pw, nw, s), "oal_beam_select")
+    return scores, parents, tokens
+
+
+def _state_of(name, t, B, Hq, Hkv, dev):
+    """Pointer of a state buffer (uint8) of B sequences; B None: as many as it has room for."""
+    if t.dtype is not torch.uint8 or t.dim() != 1:
+        raise TypeError(f"{name} must be a state buffer (uint8, one dimension)")
+    if t.device != dev or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+    empty = state_bytes(Shape(0, 1, Hq, Hkv, 64, 64, 128, OAL_BF16))
+    one = Hkv * FEATURES_PAD * (VALUE_DIM + 1) * 4
+    held = (t.numel() - empty) // one
+    if t.numel() < empty or (B is not None and held < B):
+        raise ValueError(f"{name} holds {t.numel()} bytes, too few for its sequences")
+    return t.data_ptr(), held
+
+
+def state_reorder(src, parents, dst, Hq: int, Hkv: int, stream=None):
+    """oal_state_reorder: sequence i of the state buffer dst becomes sequence parents[i] (int32)
+    of the state buffer src; dst has as many sequences as there are parents.  Returns dst."""
+    dev = src.device
+    B = parents.numel()
+    psrc, n = _state_of("src", src, None, Hq, Hkv, dev)
+    pdst, _ = _state_of("dst", dst, B, Hq, Hkv, dev)
+    ppar = _parents(parents, B, dev)
+    shape = Shape(B, 1, Hq, Hkv, 64, 64, 128, OAL_BF16)
+    with _on(dev, stream) as s:
+        _check(lib().oal_state_reorder(psrc, n, ppar, pdst, ctypes.byref(shape), s),
+               "oal_state_reorder")
+    return dst
+
+
+def decay_state_reorder(src, parents, dst, stream=None):
+    """oal_decay_state_reorder: dst[i] = src[parents[i]] for states [B, Hkv, 64, 64] fp32."""
+    dev = src.device
+    B, Hkv = parents.numel(), src.shape[1]
+    psrc = _need("src", src, (src.shape[0], Hkv, 64, 64), torch.float32, dev)
+    pdst = _need("dst", dst, (B, Hkv, 64, 64), torch.float32, dev)
+    ppar = _parents(parents, B, dev)
+    shape = Shape(B, 1, Hkv, Hkv, 64, 64, 128, OAL_BF16)
+    with _on(dev, stream) as s:
+        _check(lib().oal_decay_state_reorder(psrc, src.shape[0], ppar, pdst, ctypes.byref(shape),
+                                             s), "oal_decay_state_reorder")
+    return dst
+
+
+def decode_step_beam(q, k, v, src, parents, dst, workspace, out=None, stream=None):
+    """oal_decode_step_beam: a decode step of sequence i from sequence parents[i] (int32) of the
+    state buffer src, into the state buffer dst; returns out [B, Hq, 1, 64] fp32."""
+    shape = _shape_of(q, k, v, 128)
+    B, Hq, T, d = q.shape
+    Hkv, dev = shape.Hkv, q.device
+    if T != 1:
+        raise ValueError("decode_step_beam takes one token: q, k, v [B, H, 1, 64]")
+    pq = _need("q", q, q.shape, q.dtype, dev)
+    pk = _need("k", k, (B, Hkv, 1, d), q.dtype, dev)
+    pv = _need("v", v, (B, Hkv, 1, d), q.dtype, dev)
+    psrc, n = _state_of("src", src, None, Hq, Hkv, dev)
+    pdst, _ = _state_of("dst", dst, B, Hq, Hkv, dev)
+    ppar = _parents(parents, B, dev)
+    pw, nw = _need_ws(workspace, dev)
+    with _on(dev, stream) as s:
+        if out is None:
+            out = torch.empty(B, Hq, 1, d, dtype=torch.float32, device=dev)
+        _check(lib().oal_decode_step_beam(
+            pq, pk, pv, psrc, n, ppar, pdst,
+            _need("out", out, (B, Hq, 1, d), torch.float32, dev), pw, nw, ctypes.byref(shape), s),
+            "oal_decode_step_beam")
+    return out
 
 
 def launch_count() -> int:
