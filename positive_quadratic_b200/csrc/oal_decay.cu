@@ -4,6 +4,7 @@
 
 #include "oal_common.cuh"
 #include "oal_decay.cuh"
+#include "oal_decay_tc.cuh"
 #include "oal_kernels.cuh"
 
 namespace oal {
@@ -13,17 +14,15 @@ constexpr int kC = 64;          // tokens per chunk of the fp32 kernels
 constexpr int kThreads = 256;
 constexpr int kLd = kD + 4;     // padded row: 16-byte reads of 8 consecutive rows touch all banks
 
-// Rows [t0, t0 + n) of head plane `src` as fp32 into a [64][kLd] tile, zero from row n on.
-template <typename T>
-__device__ __forceinline__ void load_tile(float (*dst)[kLd], const T* src, int t0, int n,
+// Rows [t0, t0 + n) of head plane `src` into a [64][kLd] tile, zero from row n on.
+__device__ __forceinline__ void load_tile(float (*dst)[kLd], const float* src, int t0, int n,
                                           const float* row_scale = nullptr)
 {
     for (int e = threadIdx.x; e < kC * kD / 4; e += kThreads) {
         const int r = e / (kD / 4), c = 4 * (e % (kD / 4));
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         if (r < n) {
-            const T* p = src + size_t(t0 + r) * kD + c;
-            a = make_float4(to_f32(p[0]), to_f32(p[1]), to_f32(p[2]), to_f32(p[3]));
+            a = *reinterpret_cast<const float4*>(src + size_t(t0 + r) * kD + c);
             if (row_scale) {
                 const float w = row_scale[r];
                 a = make_float4(a.x * w, a.y * w, a.z * w, a.w * w);
@@ -37,11 +36,11 @@ __device__ __forceinline__ void load_tile(float (*dst)[kLd], const T* src, int t
 // E_c of one (chunk, kv, b): a 64 x 64 product over the chunk's tokens, for every y head of the
 // kv head.  Thread (ty, tx) owns rows 4 ty .. + 3 and columns 4 tx .. + 3.
 // ------------------------------------------------------------------------------------------
-template <typename T>
 __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, DecaySum a, DecaySum b2)
 {
     const DecaySum& J = blockIdx.z ? b2 : a;
     const int c = blockIdx.x, bkv = blockIdx.y, b = bkv / S.Hkv, kv = bkv % S.Hkv;
+    tc::grid_dep_launch();
     const int n = min(kC, decay_len(S, b) - c * kC);
     if (n <= 0) return;  // the scan does not read it
     __shared__ __align__(16) float Y[kC][kLd], Z[kC][kLd];
@@ -55,8 +54,8 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
     for (int h = 0; h < grp; ++h) {
         const size_t plane = (size_t(b) * J.hy + kv * grp + h) * S.T * kD;
         __syncthreads();
-        load_tile(Y, static_cast<const T*>(J.y) + plane, c * kC, n, w);
-        load_tile(Z, static_cast<const T*>(J.z) + plane, c * kC, n);
+        load_tile(Y, static_cast<const float*>(J.y) + plane, c * kC, n, w);
+        load_tile(Z, static_cast<const float*>(J.z) + plane, c * kC, n);
         __syncthreads();
 #pragma unroll 4
         for (int j = 0; j < kC; ++j) {
@@ -77,59 +76,122 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
 }
 
 // ------------------------------------------------------------------------------------------
-// The scan over chunks of every (b, kv): thread = one state entry.
+// The scan over the chunks of every (b, kv): cur <- l^n cur + E_c, cur written before each.
+// Block = 64 state entries (two per lane) and up to 64 chunks at a time, 8 per warp: a warp sums
+// its 8 chunks by themselves, all of them loaded at once, then starts over from what the warps
+// before it leave.  One round trip to memory for 64 chunks instead of 64.
 // ------------------------------------------------------------------------------------------
+constexpr int kScanCols = 64, kScanRun = 8;
+
+__device__ __forceinline__ void store2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
+__device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v)
+{
+    *reinterpret_cast<uint32_t*>(p) = tc::pack_bf16x2(v.x, v.y);
+}
+__device__ __forceinline__ float2 fma_decay(float l, float2 cur, float2 d)
+{
+    return make_float2(fmaf(l, cur.x, d.x), fmaf(l, cur.y, d.y));
+}
+
 template <typename Tm>
 __global__ void __launch_bounds__(kThreads) scan_kernel(DecayShape S, DecaySum a, DecaySum b2,
                                                         int chunk)
 {
     const DecaySum& J = blockIdx.z ? b2 : a;
     const int bkv = blockIdx.y, b = bkv / S.Hkv, kv = bkv % S.Hkv;
-    const int e = blockIdx.x * kThreads + threadIdx.x;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int e = blockIdx.x * kScanCols + 2 * lane;
+    __shared__ float2 tot[8][32];
+    __shared__ float pw[8];
+    tc::grid_dep_launch();
     const int len = decay_len(S, b);
-    const int nc = (len + chunk - 1) / chunk;
+    const int nc = (len + chunk - 1) / chunk, tail = len - (nc - 1) * chunk;
     const float g = decay_log(S.log_decay, kv);
-    const float full = decay_pow(g, chunk), tail = decay_pow(g, len - (nc - 1) * chunk);
-    const size_t base = size_t(bkv) * S.chunks * kDecayState + e;
-    float cur = J.first ? J.first[size_t(bkv) * kDecayState + e] : 0.f;
-    for (int i = 0; i < nc; ++i) {
-        const int c = J.rev ? nc - 1 - i : i;
-        const size_t at = base + size_t(c) * kDecayState;
-        const float d = J.delta[at];
-        static_cast<Tm*>(J.mem)[at] = Tm(cur);
-        cur = fmaf(c == nc - 1 ? tail : full, cur, d);
+    const float l_full = decay_pow(g, chunk), l_tail = decay_pow(g, tail);
+    const size_t plane = (size_t(bkv) * S.chunks) * kDecayState + e;
+    const size_t part = size_t(S.B) * S.Hkv * S.chunks * kDecayState;
+    tc::grid_dep_wait();
+    float2 cur = make_float2(0.f, 0.f);
+    if (J.first)
+        cur = *reinterpret_cast<const float2*>(J.first + size_t(bkv) * kDecayState + e);
+    for (int base = 0; base < nc; base += 8 * kScanRun) {
+        const int i0 = base + warp * kScanRun, cnt = max(0, min(kScanRun, nc - i0));
+        auto chunk_at = [&](int i) { return J.rev ? nc - 1 - (i0 + i) : i0 + i; };
+        auto decay_at = [&](int i) { return chunk_at(i) == nc - 1 ? l_tail : l_full; };
+        float2 d[kScanRun];
+#pragma unroll
+        for (int i = 0; i < kScanRun; ++i)
+            if (i < cnt)
+                d[i] = *reinterpret_cast<const float2*>(J.delta + plane +
+                                                        size_t(chunk_at(i)) * kDecayState);
+        for (int p = 1; p < J.parts; ++p) {
+#pragma unroll
+            for (int i = 0; i < kScanRun; ++i)
+                if (i < cnt) {
+                    const float2 x = *reinterpret_cast<const float2*>(
+                        J.delta + p * part + plane + size_t(chunk_at(i)) * kDecayState);
+                    d[i].x += x.x;
+                    d[i].y += x.y;
+                }
+        }
+        float2 sum = make_float2(0.f, 0.f);
+        int tokens = 0;
+#pragma unroll
+        for (int i = 0; i < kScanRun; ++i)
+            if (i < cnt) {
+                sum = fma_decay(decay_at(i), sum, d[i]);
+                tokens += chunk_at(i) == nc - 1 ? tail : chunk;
+            }
+        tot[warp][lane] = sum;
+        if (lane == 0) pw[warp] = decay_pow(g, tokens);
+        __syncthreads();
+        float2 mine = cur;
+#pragma unroll
+        for (int w = 0; w < 8; ++w) {
+            if (w == warp) mine = cur;
+            cur = fma_decay(pw[w], cur, tot[w][lane]);
+        }
+#pragma unroll
+        for (int i = 0; i < kScanRun; ++i)
+            if (i < cnt) {
+                store2(static_cast<Tm*>(J.mem) + plane + size_t(chunk_at(i)) * kDecayState, mine);
+                mine = fma_decay(decay_at(i), mine, d[i]);
+            }
+        __syncthreads();
     }
-    if (J.last) J.last[size_t(bkv) * kDecayState + e] = cur;
+    if (J.last && warp == 0) store2(J.last + size_t(bkv) * kDecayState + e, cur);
 }
 
 // ------------------------------------------------------------------------------------------
 // The mix of one (chunk, x head, b).  Thread (ty, tx) owns rows 4 ty .. + 3; of the scores the
 // columns tx + 16 e (conflict-free reads of y rows), of the output the columns 4 tx .. + 3.
 // ------------------------------------------------------------------------------------------
-template <typename T>
 struct MixSmem {
     float X[kC][kLd], Y[kC][kLd], Z[kC][kLd], P[kC][kLd];
     float pw[kC + 1];  // powers of l
 };
 
-template <typename T>
 __global__ void __launch_bounds__(kThreads) mix_simt_kernel(DecayShape S, DecayJob j0, DecayJob j1,
                                                             DecayJob j2)
 {
     extern __shared__ __align__(16) unsigned char smem_raw[];
-    MixSmem<T>& sm = *reinterpret_cast<MixSmem<T>*>(smem_raw);
+    MixSmem& sm = *reinterpret_cast<MixSmem*>(smem_raw);
     const DecayJob& J = blockIdx.z == 0 ? j0 : blockIdx.z == 1 ? j1 : j2;
     const int c = blockIdx.x, b = blockIdx.y / J.hx, hx = blockIdx.y % J.hx;
-    if (b >= S.B) return;  // the jobs share a grid of the largest head count
-    const int n = min(kC, decay_len(S, b) - c * kC);
-    if (n <= 0) return;
+    // the jobs share a grid of the largest head count
+    const int n = b < S.B ? min(kC, decay_len(S, b) - c * kC) : 0;
+    if (n <= 0) {
+        tc::grid_dep_wait();  // as every block does: the kernel ends after the ones before it
+        return;
+    }
     const int kv = hx * S.Hkv / J.hx;
     const int nh = J.hy > J.hx ? J.hy / J.hx : 1;
     const int y0 = J.hy > J.hx ? hx * nh : hx * J.hy / J.hx;
     const float g = decay_log(S.log_decay, kv);
     for (int e = threadIdx.x; e <= kC; e += kThreads) sm.pw[e] = decay_pow(g, e);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    load_tile(sm.X, static_cast<const T*>(J.x) + (size_t(b) * J.hx + hx) * S.T * kD, c * kC, n);
+    load_tile(sm.X, static_cast<const float*>(J.x) + (size_t(b) * J.hx + hx) * S.T * kD, c * kC, n);
+    tc::grid_dep_wait();
     // M (or its transpose) where Z goes later
     const float* M = static_cast<const float*>(J.mem) +
                      ((size_t(b) * S.Hkv + kv) * S.chunks + c) * kDecayState;
@@ -166,8 +228,8 @@ __global__ void __launch_bounds__(kThreads) mix_simt_kernel(DecayShape S, DecayJ
     for (int h = 0; h < nh; ++h) {
         const size_t plane = (size_t(b) * J.hy + y0 + h) * S.T * kD;
         __syncthreads();
-        load_tile(sm.Y, static_cast<const T*>(J.y) + plane, c * kC, n);
-        load_tile(sm.Z, static_cast<const T*>(J.z) + plane, c * kC, n);
+        load_tile(sm.Y, static_cast<const float*>(J.y) + plane, c * kC, n);
+        load_tile(sm.Z, static_cast<const float*>(J.z) + plane, c * kC, n);
         __syncthreads();
         float s[4][4] = {};
 #pragma unroll 2
@@ -199,15 +261,15 @@ __global__ void __launch_bounds__(kThreads) mix_simt_kernel(DecayShape S, DecayJ
         __syncthreads();
         product(sm.P, sm.Z, near);
     }
-    T* out = static_cast<T*>(J.out) + ((size_t(b) * J.hx + hx) * S.T + c * kC) * kD;
+    float* out = static_cast<float*>(J.out) + ((size_t(b) * J.hx + hx) * S.T + c * kC) * kD;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = 4 * ty + i;
         if (row >= n) continue;
         const float bi = J.rev ? sm.pw[n - 1 - row] : S.scale * sm.pw[row + 1];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            out[size_t(row) * kD + 4 * tx + e] = T(fmaf(S.scale, near[i][e], bi * far[i][e]));
+        *reinterpret_cast<float4*>(out + size_t(row) * kD + 4 * tx) = make_float4(
+            fmaf(S.scale, near[i][0], bi * far[i][0]), fmaf(S.scale, near[i][1], bi * far[i][1]),
+            fmaf(S.scale, near[i][2], bi * far[i][2]), fmaf(S.scale, near[i][3], bi * far[i][3]));
     }
 }
 
@@ -279,13 +341,11 @@ __global__ void __launch_bounds__(kThreads) step_kernel(const T* __restrict__ q,
 }
 
 // ---- host ----------------------------------------------------------------------------------
-int chunk_of(const oal_shape*) { return kC; }
+bool on_tensor_cores(const oal_shape* s) { return s->dtype == OAL_BF16; }
 
-size_t sum_bytes(const oal_shape* s)
-{
-    const size_t nc = (size_t(s->T) + chunk_of(s) - 1) / chunk_of(s);
-    return align256(size_t(s->B) * s->Hkv * nc * kDecayState * 4);
-}
+int chunk_of(const oal_shape* s) { return on_tensor_cores(s) ? dtc::kC : kC; }
+
+int chunks_of(const oal_shape* s) { return int((s->T + (long long)chunk_of(s) - 1) / chunk_of(s)); }
 
 template <typename F>
 int by_type(int dtype, F f)
@@ -293,42 +353,154 @@ int by_type(int dtype, F f)
     return dtype == OAL_BF16 ? f(__nv_bfloat16{}) : f(float{});
 }
 
+// Parts in which the heads of a group are summed (the gradient's R): enough CTAs for two per SM
+// where the chunks alone are too few, at the price of a 16 KB partial sum each.
+constexpr int kSms = 148;
+int parts_of(const oal_shape* s, int grp)
+{
+    const long long items = (long long)s->B * s->Hkv * chunks_of(s);
+    if (!on_tensor_cores(s) || items == 0) return 1;
+    const int parts = int(std::min<long long>(grp, (2 * kSms + items - 1) / items));
+    const int per = (grp + parts - 1) / parts;
+    return (grp + per - 1) / per;  // none of them empty
+}
+
+// Workspace of one sum: the chunks' products, and (bf16) the images of the states before them.
+struct SumLayout {
+    size_t delta, mem, total;
+};
+SumLayout sum_layout(const oal_shape* s, int parts)
+{
+    const size_t states = size_t(s->B) * s->Hkv * chunks_of(s);
+    const size_t one = align256(states * kDecayState * 4);
+    SumLayout l{0, 0, one * parts};
+    if (on_tensor_cores(s)) {
+        l.mem = one * parts;
+        l.total += align256(states * kDecayState * 2);
+    }
+    return l;
+}
+
+DecaySum make_sum(const void* y, const void* z, int hy, int rev, int parts, unsigned char* ws,
+                  const oal_shape* s, const float* first, float* last)
+{
+    const SumLayout l = sum_layout(s, parts);
+    return {y, z, hy, rev, parts, reinterpret_cast<float*>(ws + l.delta), ws + l.mem, first, last};
+}
+
+cudaError_t set_attributes_once()
+{
+    constexpr int kMaxDev = 64;
+    static std::atomic<int> done[kMaxDev] = {};
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < kMaxDev && done[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const std::pair<const void*, int> smem[] = {
+        {reinterpret_cast<const void*>(dtc::delta_kernel), int(dtc::kDeltaSmem)},
+        {reinterpret_cast<const void*>(dtc::mix_kernel), int(dtc::kMixSmem)},
+        {reinterpret_cast<const void*>(mix_simt_kernel), int(sizeof(MixSmem))}};
+    for (const auto& k : smem) {
+        if ((e = cudaFuncSetAttribute(k.first, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      k.second)) != cudaSuccess ||
+            (e = cudaFuncSetAttribute(k.first, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                      100)) != cudaSuccess)
+            return e;
+    }
+    if (dev >= 0 && dev < kMaxDev) done[dev].store(1, std::memory_order_release);
+    return cudaSuccess;
+}
+
+// [heads][T][64] bf16 for copies out of 32 rows (what a pair of warps has written)
+bool make_out_map(CUtensorMap* m, const void* base, int T, int heads)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {64, cuuint64_t(T), cuuint64_t(heads)};
+    const cuuint64_t strides[2] = {64 * 2, cuuint64_t(T) * 64 * 2};
+    const cuuint32_t box[3] = {64, 32, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// [planes][64] bf16 state images of 64 rows each, as 2D {64, planes * 64}
+bool make_state_map(CUtensorMap* m, const void* base, size_t planes)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[2] = {64, cuuint64_t(planes) * 64};
+    const cuuint64_t strides[1] = {128};
+    const cuuint32_t box[2] = {64, 64};
+    const cuuint32_t estr[2] = {1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The sums of `n` directions (1 or 2) and their scans.
 int launch_sums(const DecayShape& S, const DecaySum* a, int n, const oal_shape* s, cudaStream_t st)
 {
     const DecaySum& b2 = a[n - 1];
-    if (S.chunks > 0)
-        if (const int rc = by_type(s->dtype, [&](auto t) {
-                LaunchScope ls("decay_delta", st);
-                delta_simt_kernel<decltype(t)>
-                    <<<dim3(S.chunks, s->B * s->Hkv, n), kThreads, 0, st>>>(S, a[0], b2);
-                OAL_LAUNCH_CHECK();
-                return int(OAL_OK);
-            }))
-            return rc;
+    const int planes = s->B * s->Hkv;
+    if (S.chunks > 0) {
+        LaunchScope ls("decay_delta", st);
+        if (on_tensor_cores(s)) {
+            dtc::SumMaps maps;
+            int items = 0;
+            for (int i = 0; i < 2; ++i) {
+                const DecaySum& j = i < n ? a[i] : a[0];
+                if (!make_map_uncached(&maps.y[i], j.y, s->T, s->B * j.hy) ||
+                    !make_map_uncached(&maps.z[i], j.z, s->T, s->B * j.hy))
+                    return OAL_ERR_CUDA;
+                if (i < n) items += j.parts * planes * S.chunks;
+            }
+            dtc::delta_kernel<<<items, dtc::kThreads, dtc::kDeltaSmem, st>>>(maps, S, a[0], b2);
+        } else {
+            delta_simt_kernel<<<dim3(S.chunks, planes, n), kThreads, 0, st>>>(S, a[0], b2);
+        }
+        OAL_LAUNCH_CHECK();
+    }
     LaunchScope ls("decay_scan", st);
-    scan_kernel<float><<<dim3(kDecayState / kThreads, s->B * s->Hkv, n), kThreads, 0, st>>>(
-        S, a[0], b2, chunk_of(s));
-    OAL_LAUNCH_CHECK();
+    OAL_CUDA_TRY(launch_ex(on_tensor_cores(s) ? scan_kernel<__nv_bfloat16> : scan_kernel<float>,
+                           dim3(kDecayState / kScanCols, planes, n), dim3(kThreads), 0, st,
+                           S.chunks > 0, S, a[0], b2, chunk_of(s)));
     return OAL_OK;
 }
 
-int launch_mix(const DecayShape& S, const DecayJob* j, int n, const oal_shape* s, cudaStream_t st)
+int launch_mix(const DecayShape& S, const DecayJob* j, const DecaySum* const* sums, int n,
+               const oal_shape* s, cudaStream_t st)
 {
     if (S.chunks == 0) return OAL_OK;
-    int hx = 0;
-    for (int i = 0; i < n; ++i) hx = std::max(hx, j[i].hx);
-    return by_type(s->dtype, [&](auto t) {
-        using T = decltype(t);
-        OAL_CUDA_TRY(cudaFuncSetAttribute(mix_simt_kernel<T>,
-                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          int(sizeof(MixSmem<T>))));
-        LaunchScope ls("decay_mix", st);
-        mix_simt_kernel<T><<<dim3(S.chunks, s->B * hx, n), kThreads, sizeof(MixSmem<T>), st>>>(
-            S, j[0], j[n > 1 ? 1 : 0], j[n > 2 ? 2 : 0]);
-        OAL_LAUNCH_CHECK();
-        return int(OAL_OK);
-    });
+    LaunchScope ls("decay_mix", st);
+    if (!on_tensor_cores(s)) {
+        int hx = 0;
+        for (int i = 0; i < n; ++i) hx = std::max(hx, j[i].hx);
+        OAL_CUDA_TRY(launch_ex(mix_simt_kernel, dim3(S.chunks, s->B * hx, n), dim3(kThreads),
+                               sizeof(MixSmem), st, true, S, j[0], j[n > 1 ? 1 : 0],
+                               j[n > 2 ? 2 : 0]));
+        return OAL_OK;
+    }
+    dtc::MixJobs jobs;
+    jobs.n = n;
+    long long items = 0;
+    for (int i = 0; i < n; ++i) {
+        dtc::MixJob& m = jobs.job[i];
+        m.j = j[i];
+        m.has_first = sums[i]->first != nullptr;
+        m.items = s->B * j[i].hx * S.chunks;
+        items += m.items;
+        if (!make_map_uncached(&m.x, j[i].x, s->T, s->B * j[i].hx) ||
+            !make_map_uncached(&m.y, j[i].y, s->T, s->B * j[i].hy) ||
+            !make_map_uncached(&m.z, j[i].z, s->T, s->B * j[i].hy) ||
+            !make_out_map(&m.o, j[i].out, s->T, s->B * j[i].hx) ||
+            !make_state_map(&m.m, j[i].mem, size_t(s->B) * s->Hkv * S.chunks))
+            return OAL_ERR_CUDA;
+    }
+    OAL_CUDA_TRY(launch_ex(dtc::mix_kernel, dim3(int(std::min<long long>(items, 2 * sm_count()))),
+                           dim3(dtc::kMixThreads), dtc::kMixSmem, st, true, jobs, S, int(items)));
+    return OAL_OK;
 }
 
 int check(const oal_shape* s)
@@ -357,14 +529,15 @@ int prefill(const void* q, const void* k, const void* v, const float* log_decay,
     if (!ws || ws_bytes < need) return OAL_ERR_WORKSPACE;
     if (!aligned16(ws)) return OAL_ERR_ALIGN;
     if (cont && s->T == 0) return OAL_OK;
-    const DecayShape S{s->B, s->T, s->Hkv, (s->T + chunk_of(s) - 1) / chunk_of(s), lens, log_decay,
-                       scale};
+    OAL_CUDA_TRY(set_attributes_once());
+    const DecayShape S{s->B, s->T, s->Hkv, chunks_of(s), lens, log_decay, scale};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    float* d = static_cast<float*>(ws);
-    const DecaySum sum{k, v, s->Hkv, 0, d, d, cont ? state : nullptr, state};
+    const DecaySum sum = make_sum(k, v, s->Hkv, 0, 1, static_cast<unsigned char*>(ws), s,
+                                  cont ? state : nullptr, state);
     if ((rc = launch_sums(S, &sum, 1, s, st)) || !out) return rc;
-    const DecayJob job{q, k, v, out, d, s->Hq, s->Hkv, 0, 0};
-    return launch_mix(S, &job, 1, s, st);
+    const DecayJob job{q, k, v, out, sum.mem, s->Hq, s->Hkv, 0, 0};
+    const DecaySum* of[] = {&sum};
+    return launch_mix(S, &job, of, 1, s, st);
 }
 
 }  // namespace decay
@@ -388,7 +561,7 @@ int oal_decay_prefill_workspace_bytes(const oal_shape* s, size_t* bytes)
     const int rc = decay::check(s);
     if (rc) return rc;
     if (!bytes) return OAL_ERR_NULL;
-    *bytes = std::max<size_t>(decay::sum_bytes(s), 256);
+    *bytes = std::max<size_t>(decay::sum_layout(s, 1).total, 256);
     return OAL_OK;
 }
 
@@ -451,7 +624,9 @@ int oal_decay_backward_workspace_bytes(const oal_shape* s, size_t* bytes)
     const int rc = decay::check(s);
     if (rc) return rc;
     if (!bytes) return OAL_ERR_NULL;
-    *bytes = std::max<size_t>(2 * decay::sum_bytes(s), 256);
+    *bytes = std::max<size_t>(decay::sum_layout(s, 1).total +
+                                  decay::sum_layout(s, decay::parts_of(s, s->Hq / s->Hkv)).total,
+                              256);
     return OAL_OK;
 }
 
@@ -472,19 +647,21 @@ int oal_decay_backward(const void* q, const void* k, const void* v, const float*
     if ((rc = oal_decay_backward_workspace_bytes(s, &need))) return rc;
     if (!workspace || workspace_bytes < need) return OAL_ERR_WORKSPACE;
     if (!aligned16(workspace)) return OAL_ERR_ALIGN;
-    const int C = decay::chunk_of(s);
-    const DecayShape S{s->B, s->T, s->Hkv, (s->T + C - 1) / C, lens, log_decay, scale};
+    OAL_CUDA_TRY(decay::set_attributes_once());
+    const DecayShape S{s->B, s->T, s->Hkv, decay::chunks_of(s), lens, log_decay, scale};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     unsigned char* w = static_cast<unsigned char*>(workspace);
-    float* fs = reinterpret_cast<float*>(w);
-    float* rs = reinterpret_cast<float*>(w + decay::sum_bytes(s));
-    const DecaySum sums[2] = {{k, v, s->Hkv, 0, fs, fs, state, nullptr},
-                              {q, dout, s->Hq, 1, rs, rs, dlast, dstate}};
+    const DecaySum sums[2] = {
+        decay::make_sum(k, v, s->Hkv, 0, 1, w, s, state, nullptr),
+        decay::make_sum(q, dout, s->Hq, 1, decay::parts_of(s, s->Hq / s->Hkv),
+                        w + decay::sum_layout(s, 1).total, s, dlast, dstate)};
     if ((rc = decay::launch_sums(S, sums, 2, s, st))) return rc;
-    const DecayJob jobs[3] = {{dout, v, k, dq, fs, s->Hq, s->Hkv, 0, 1},
-                              {v, dout, q, dk, rs, s->Hkv, s->Hq, 1, 1},
-                              {k, q, dout, dv, rs, s->Hkv, s->Hq, 1, 0}};
-    return decay::launch_mix(S, jobs, 3, s, st);
+    // the long items (every head of a group) first
+    const DecayJob jobs[3] = {{v, dout, q, dk, sums[1].mem, s->Hkv, s->Hq, 1, 1},
+                              {k, q, dout, dv, sums[1].mem, s->Hkv, s->Hq, 1, 0},
+                              {dout, v, k, dq, sums[0].mem, s->Hq, s->Hkv, 0, 1}};
+    const DecaySum* const of[3] = {&sums[1], &sums[1], &sums[0]};
+    return decay::launch_mix(S, jobs, of, 3, s, st);
 }
 
 }  // extern "C"

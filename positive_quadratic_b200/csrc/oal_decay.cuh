@@ -45,8 +45,9 @@ struct DecaySum {
     const void* z;
     int hy;
     int rev;
-    float* delta;        // [B * Hkv][chunks][64][64]
-    void* mem;           // the same, fp32 (may be `delta`) or bf16
+    int parts;           // the heads of a group are summed in so many parts, joined by the scan
+    float* delta;        // [parts][B * Hkv][chunks][64][64]
+    void* mem;           // [B * Hkv][chunks][64][64], fp32 (may be `delta`) or bf16
     const float* first;  // [B * Hkv][64][64], or NULL for zero
     float* last;         // the total, or NULL
 };

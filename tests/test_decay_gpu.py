@@ -30,7 +30,7 @@ def clean():
 
 SHAPES = [(1, 1, 1, 1), (2, 2, 2, 1), (1, 63, 7, 1), (2, 64, 6, 3), (1, 65, 8, 1), (3, 127, 2, 2),
           (1, 128, 14, 2), (2, 129, 4, 4), (1, 255, 3, 1), (2, 300, 14, 2), (1, 1000, 5, 5),
-          (1, 2049, 4, 2)]
+          (1, 2049, 4, 2), (1, 1000, 56, 8)]  # the last: a group of 7 summed in uneven parts
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
