@@ -63,7 +63,7 @@ struct DecayShape {
 // device sees.  exp(-1e4) is 0 in fp32, so that a decay of 0 (log -inf) keeps l^0 = 1.
 __device__ __forceinline__ float decay_log(const float* log_decay, int kv)
 {
-    const float g = log_decay[kv];
+    const float g = __ldg(log_decay + kv);
     if (!(g <= 0.f)) {
         raise_error(OAL_ERR_VALUE);
         return 0.f;
@@ -83,7 +83,7 @@ __device__ __forceinline__ float decay_pow(float g, int m)
 __device__ __forceinline__ int decay_len(const DecayShape& s, int b)
 {
     if (!s.lens) return s.T;
-    const int n = s.lens[b];
+    const int n = __ldg(s.lens + b);
     if (n < 0 || n > s.T) {
         raise_error(OAL_ERR_VALUE);
         return n < 0 ? 0 : s.T;

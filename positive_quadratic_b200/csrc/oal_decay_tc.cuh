@@ -15,7 +15,7 @@ namespace dtc {
 using namespace oal::tc;  // PTX layer
 
 constexpr int kC = 128;
-constexpr int kThreads = 288;   // 8 compute warps and one that issues copies and MMAs
+constexpr int kThreads = 288;   // of the delta kernel: 8 compute warps and a control warp
 constexpr int kCtrlWarp = 8;
 constexpr uint32_t kTile = kC * 128;      // a 128 x 64 bf16 tile
 constexpr uint32_t kMTile = 64 * 128;     // a 64 x 64 bf16 state image
@@ -49,17 +49,11 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
         : "memory");
 }
 
-__device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, int x, int y, int z)
-{
-    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
-                 ::"l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
-                 : "memory");
-}
-
-// Rows [n, 128) of a tile to zero, by the 256 compute threads.
+// Rows [n, 128) of a tile to zero, by the first kBy threads.
+template <int kBy>
 __device__ __forceinline__ void zero_rows(unsigned char* tile, int n)
 {
-    for (int e = n * 8 + threadIdx.x; e < kC * 8; e += 256)
+    for (int e = n * 8 + threadIdx.x; e < kC * 8; e += kBy)
         *reinterpret_cast<uint4*>(tile + e * 16) = make_uint4(0, 0, 0, 0);
 }
 
@@ -90,8 +84,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     delta_kernel(const __grid_constant__ SumMaps maps, DecayShape S, DecaySum a, DecaySum b2)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char* sm = reinterpret_cast<unsigned char*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* sm = smem_raw + (-smem_u32(smem_raw) & 1023u);  // still known to be shared
     DeltaCtl& ctl = *reinterpret_cast<DeltaCtl*>(sm + kDOffCtl);
     volatile int* abort_flag = &ctl.abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -163,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     sts128(lo + 2 * kTile + off, p[1][0], p[1][1], p[1][2], p[1][3]);
                     sts128(lo + off, p[2][0], p[2][1], p[2][2], p[2][3]);
                 }
-                if (n < kC) zero_rows(sm + kDOffZ + (i & 1) * kTile, n);
+                if (n < kC) zero_rows<256>(sm + kDOffZ + (i & 1) * kTile, n);
                 fence_proxy_async();
                 warp_arrive(&ctl.parts);
             }
@@ -268,14 +261,15 @@ __global__ void __launch_bounds__(kThreads, 2)
 //   S_h = X Y_h^T (tensor memory), P_h = bf16(S_h o D) written over it, U = sum_h P_h Z_h,
 //   F = X M (the bf16 state before the chunk), out = scale U + b F.
 // The decay of the far part is applied to F's rows in fp32, so that q and S are rounded once.
-// Persistent: two CTAs per SM, each walking items blockIdx.x, blockIdx.x + gridDim.x, ...  The
-// control warp loads the next step's Y and Z while the present one is worked on, and issues the
-// next item's scores while the compute warps write out the present one's result.
-// Compute warp (qw, kh): rows 32 qw .. + 31 (its tensor-memory lanes) and keys 64 kh .. + 63 of
-// the scores, columns 32 kh .. + 31 of the output.
+// Persistent: two CTAs per SM, each walking items blockIdx.x, blockIdx.x + gridDim.x, ...
+// Warps 0-7 compute: warp (qw, kh) holds rows 32 qw .. + 31 (its tensor-memory lanes), keys
+// 64 kh .. + 63 of the scores and columns 32 kh .. + 31 of the output.  Warp 8 issues the MMAs;
+// the next item's scores are formed while the compute warps write out the present one's result.
+// Warp 9 looks ahead: it works out the next items' places and powers of l and loads their tiles
+// as soon as buffers are free.
 // ------------------------------------------------------------------------------------------
 struct MixJob {
-    CUtensorMap x, y, z, m, o;
+    CUtensorMap x, y, z, m;
     DecayJob j;
     int has_first;  // the chunk at the start of the scan has a state, too
     int items;      // of this job
@@ -285,35 +279,36 @@ struct MixJobs {
     int n;
 };
 
-constexpr int kMixThreads = 320;  // the compute warps, the control warp and one that looks ahead
-constexpr int kAheadWarp = 9;
+constexpr int kMixWarps = 8;  // compute warps
+constexpr int kMixThreads = (kMixWarps + 2) * 32;
+constexpr int kMmaWarp = kMixWarps, kAheadWarp = kMixWarps + 1;
+constexpr int kInfos = 4;  // items that the look-ahead warp may have described and not seen done
 
-// What the compute warps need to know of an item, and the powers of l, prepared by the look-ahead
-// warp while they work on the item before (two buffers, by the item's parity).  l^i is at
-// pw[1 + i]: pairs that start at an odd power are 8-byte aligned.
+// What the other warps need to know of an item, and the powers of l: l^i at pw[kPw0 + i], so that
+// pairs that start at an odd power are 8-byte aligned and 31 places lie before the first.
+constexpr int kPw0 = 33;
 struct MixInfo {
-    __nv_bfloat16* out;    // the tile's first row
-    const CUtensorMap* o;  // for the copy out; NULL: rows behind the sequence's end may not be written
-    int n, nh, rev, has_m, t0, plane, garbage, none;
-    float pw[132];
+    __nv_bfloat16* out;  // the tile's first row
+    int n, nh, rev, has_m, mem_t, garbage, none, pad;
+    float pw[kPw0 + kC + 3];
 };
 
 struct MixCtl {
-    uint64_t x_full, m_full, yz_full[2], s_full, p_full, pv_done, x_free, out_free;
-    uint64_t info_full[2], info_free[2];
+    uint64_t x_full, m_full, yz_full[2], yz_free[2], s_full, p_full, pv_done, x_free, out_free;
+    uint64_t info_full[kInfos], info_free[kInfos];
     uint32_t tmem_base;
     int abort_flag;
 };
 
-constexpr uint32_t kMOffX = 0, kMOffYZ = kTile, kMOffM = 5 * kTile, kMOffO = kMOffM + kMTile;
-constexpr uint32_t kMOffInfo = kMOffO + kTile;
-constexpr uint32_t kMOffCtl = kMOffInfo + 2 * sizeof(MixInfo);
-constexpr uint32_t kMixSmem = kMOffCtl + 128 + 1024;
+constexpr uint32_t kMOffX = 0, kMOffYZ = kTile, kMOffM = 5 * kTile;
+constexpr uint32_t kMOffInfo = kMOffM + kMTile;
+constexpr uint32_t kMOffCtl = kMOffInfo + kInfos * sizeof(MixInfo);
+constexpr uint32_t kMixSmem = kMOffCtl + 256 + 1024;
 constexpr uint32_t kMixTmem = 256;
 constexpr uint32_t kColS = 0, kColU = 128, kColF = 192;
-static_assert(sizeof(MixCtl) <= 128 && kMOffCtl % 8 == 0 && 2 * (kMixSmem + 1024) <= 233472,
+static_assert(sizeof(MixCtl) <= 256 && kMOffCtl % 8 == 0 && 2 * (kMixSmem + 1024) <= 233472,
               "two CTAs per SM");
-static_assert(sizeof(MixInfo) % 16 == 0 && offsetof(MixInfo, pw) % 8 == 0, "alignment of pw");
+static_assert(sizeof(MixInfo) % 8 == 0 && offsetof(MixInfo, pw) % 8 == 0 && kPw0 % 2 == 1, "alignment of pw");
 
 struct MixItem {
     int w, b, hx, kv, c, n, nh, y0, has_m;
@@ -341,64 +336,75 @@ __device__ __forceinline__ MixItem mix_item(const MixJobs& jobs, const DecayShap
     return it;
 }
 
-// P = S o D for 32 rows (lane + 32 qw) and keys 64 kh .. + 63, written over the scores.
+// P = S o D for rows 32 qw + lane and keys 32 jb .. + 31, written over the scores.
 template <bool kRev>
-__device__ __forceinline__ void decay_scores(uint32_t scores, const float* pw, int qw, int kh,
+__device__ __forceinline__ void decay_scores(uint32_t scores, const float* pw, int qw, int jb,
                                              int lane, int n)
 {
+    uint32_t p[16];
+    if (jb == qw) {  // the diagonal block
+        float s[32];
+        tmem_ld32(scores, s);
+        tmem_ld_wait();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        const int jb = 2 * kh + half;  // keys 32 jb .. + 31
-        uint32_t p[16];
-        if (jb == qw) {  // the diagonal block
-            float s[32];
-            tmem_ld32(scores + 32 * half, s);
-            tmem_ld_wait();
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-                const float d = pw[1 + ((kRev ? x - lane : lane - x) & 31)];
-                s[x] = (kRev ? x >= lane && 32 * jb + x < n : x <= lane) ? s[x] * d : 0.f;
-            }
-#pragma unroll
-            for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(s[2 * x], s[2 * x + 1]);
-        } else if (kRev ? jb > qw : jb < qw) {
-            // l^|i-j| = l^(from the row to its block's edge) l^(from there to j)
-            float s[32];
-            tmem_ld32(scores + 32 * half, s);
-            const float rf = pw[1 + (kRev ? 31 - lane : lane)];
-            const float2 rf2 = make_float2(rf, rf);
-            // the pair of columns (x, x + 1): powers at + x and at + x + 1 (kRev), or - x, - x - 1
-            const float* at = kRev ? pw + 1 + 32 * (jb - qw) - 31 : pw + 1 + 32 * (qw - jb) - 1;
-            tmem_ld_wait();
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-                float2 d = *reinterpret_cast<const float2*>(kRev ? at + x : at - x);
-                if (!kRev) d = make_float2(d.y, d.x);
-                const float2 v = __fmul2_rn(make_float2(s[x], s[x + 1]), __fmul2_rn(rf2, d));
-                s[x] = v.x;
-                s[x + 1] = v.y;
-            }
-            if (kRev && n < kC)  // keys behind the sequence's end, whatever they gave
-#pragma unroll
-                for (int x = 0; x < 32; ++x)
-                    if (32 * jb + x >= n) s[x] = 0.f;
-#pragma unroll
-            for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(s[2 * x], s[2 * x + 1]);
-        } else {
-#pragma unroll
-            for (int x = 0; x < 16; ++x) p[x] = 0u;
+        for (int x = 0; x < 32; ++x) {
+            // on the wrong side of the diagonal the factor is whatever lies there, and the
+            // product (which may be NaN, as may what lies behind the end) is not taken
+            const float d = kRev ? pw[kPw0 + x - lane] : pw[kPw0 + lane - x];
+            const float v = s[x] * d;
+            s[x] = (kRev ? x >= lane && 32 * jb + x < n : x <= lane) ? v : 0.f;
         }
-        tmem_st16(scores + 16 * half, p);  // over this warp's own scores, which it has read
+#pragma unroll
+        for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(s[2 * x], s[2 * x + 1]);
+    } else if (kRev ? jb > qw : jb < qw) {
+        // l^|i-j| = l^(from the row to its block's edge) l^(from there to j)
+        float s[32];
+        tmem_ld32(scores, s);
+        const float rf = pw[kPw0 + (kRev ? 31 - lane : lane)];
+        const float2 rf2 = make_float2(rf, rf);
+        // the pair of columns (x, x + 1): powers at + x and at + x + 1 (kRev), or - x, - x - 1
+        const float* at = pw + kPw0 + (kRev ? 32 * (jb - qw) - 31 : 32 * (qw - jb) - 1);
+        tmem_ld_wait();
+#pragma unroll
+        for (int x = 0; x < 32; x += 2) {
+            float2 d = *reinterpret_cast<const float2*>(kRev ? at + x : at - x);
+            if (!kRev) d = make_float2(d.y, d.x);
+            const float2 v = __fmul2_rn(make_float2(s[x], s[x + 1]), __fmul2_rn(rf2, d));
+            s[x] = v.x;
+            s[x + 1] = v.y;
+        }
+        if (kRev && n < kC)  // keys behind the sequence's end, whatever they gave
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+                if (32 * jb + x >= n) s[x] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(s[2 * x], s[2 * x + 1]);
+    } else {
+#pragma unroll
+        for (int x = 0; x < 16; ++x) p[x] = 0u;
     }
-    tmem_st_wait();
+    tmem_st16(scores, p);
+}
+
+// Stores 16 bf16 values (32 bytes; one store where the address allows it).
+__device__ __forceinline__ void store16(__nv_bfloat16* out, const uint32_t (&p)[8], bool wide)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out),
+                     "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]), "r"(p[4]), "r"(p[5]), "r"(p[6]),
+                     "r"(p[7])
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4*>(out)[0] = make_uint4(p[0], p[1], p[2], p[3]);
+        reinterpret_cast<uint4*>(out)[1] = make_uint4(p[4], p[5], p[6], p[7]);
+    }
 }
 
 __global__ void __launch_bounds__(kMixThreads, 2)
     mix_kernel(const __grid_constant__ MixJobs jobs, DecayShape S, int items)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
-    unsigned char* sm = reinterpret_cast<unsigned char*>(
-        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    unsigned char* sm = smem_raw + (-smem_u32(smem_raw) & 1023u);  // still known to be shared
     MixCtl& ctl = *reinterpret_cast<MixCtl*>(sm + kMOffCtl);
     MixInfo* infos = reinterpret_cast<MixInfo*>(sm + kMOffInfo);
     volatile int* abort_flag = &ctl.abort_flag;
@@ -408,19 +414,22 @@ __global__ void __launch_bounds__(kMixThreads, 2)
         mbar_init(&ctl.x_full, 1);
         mbar_init(&ctl.m_full, 1);
         mbar_init(&ctl.s_full, 1);
-        mbar_init(&ctl.p_full, 8);
+        mbar_init(&ctl.p_full, kMixWarps);
         mbar_init(&ctl.pv_done, 1);
         mbar_init(&ctl.x_free, 1);
-        mbar_init(&ctl.out_free, 8);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&ctl.yz_full[i], 1);
+        mbar_init(&ctl.out_free, kMixWarps);
+        mbar_init(&ctl.yz_full[0], 1);
+        mbar_init(&ctl.yz_full[1], 1);
+        mbar_init(&ctl.yz_free[0], 1);
+        mbar_init(&ctl.yz_free[1], 1);
+        for (int i = 0; i < kInfos; ++i) {
             mbar_init(&ctl.info_full[i], 1);
-            mbar_init(&ctl.info_free[i], 8);
+            mbar_init(&ctl.info_free[i], kMixWarps);
         }
         ctl.abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == kCtrlWarp) {
+    if (warp == kMmaWarp) {
         tmem_alloc(&ctl.tmem_base, kMixTmem);
         tmem_relinquish();
     }
@@ -429,163 +438,167 @@ __global__ void __launch_bounds__(kMixThreads, 2)
     tc_fence_after();
     const uint32_t tmem = ctl.tmem_base;
 
-    if (warp < 8) {
+    if (warp < kMixWarps) {
         const int qw = warp & 3, kh = warp >> 2, row = 32 * qw + lane;
         const uint32_t lanes = tmem + (uint32_t(qw * 32) << 16);
-        // the two warps of 32 rows agree once per item whether to go on: a wait that ran out in
-        // one must not leave the other at their barrier
-        for (int done = 0, step = 0;; ++done) {
-            bool ok = wait_all(&ctl.info_full[done & 1], (done >> 1) & 1, abort_flag);
-            const MixInfo& I = infos[done & 1];
-            ok = ok && !I.none;
+        bool ok = true;
+        for (int done = 0, step = 0; ok; ++done) {
+            ok = wait_all(&ctl.info_full[done % kInfos], (done / kInfos) & 1, abort_flag);
+            const MixInfo& I = infos[done % kInfos];
+            if (!ok || I.none) break;
             const int n = I.n, nh = I.nh, rev = I.rev, has_m = I.has_m;
-            for (int h = 0; ok && h < nh; ++h, ++step) {
+            for (int h = 0; h < nh; ++h, ++step) {
                 ok = wait_all(&ctl.s_full, step & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-                if (rev) decay_scores<true>(lanes + kColS + 64 * kh, I.pw, qw, kh, lane, n);
-                else decay_scores<false>(lanes + kColS + 64 * kh, I.pw, qw, kh, lane, n);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int jb = 2 * kh + half;
+                    if (rev) decay_scores<true>(lanes + kColS + 32 * jb, I.pw, qw, jb, lane, n);
+                    else decay_scores<false>(lanes + kColS + 32 * jb, I.pw, qw, jb, lane, n);
+                }
+                tmem_st_wait();
                 tc_fence_before();
                 if (I.garbage) {
                     // rows behind the sequence's end: zero times what lies there has to be zero
                     ok = wait_all(&ctl.yz_full[step & 1], (step >> 1) & 1, abort_flag);
                     if (!ok) break;
-                    zero_rows(sm + kMOffYZ + (step & 1) * 2 * kTile + kTile, n);
+                    zero_rows<kMixWarps * 32>(sm + kMOffYZ + (step & 1) * 2 * kTile + kTile, n);
                     fence_proxy_async();
                 }
                 warp_arrive(&ctl.p_full);
             }
+            const float bi = rev ? (row < n ? I.pw[kPw0 + n - 1 - row] : 0.f)
+                                 : S.scale * I.pw[kPw0 + row + 1];
+            __nv_bfloat16* out = I.out + row * kD + 32 * kh;
             ok = ok && wait_all(&ctl.pv_done, (step - 1) & 1, abort_flag);
-            if (lane == 0 && kh == 0) bulk_wait_read0();  // the copy before has read these rows
-            if (!named_bar_and(1 + qw, 64, ok)) break;
-            const float bi = rev ? (row < n ? I.pw[n - row] : 0.f) : S.scale * I.pw[row + 2];
-            const uint32_t o = smem_u32(sm + kMOffO);
-            const bool copied = I.o != nullptr;
+            if (!ok) break;
             tc_fence_after();
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                float u[16], f[16];
-                tmem_ld16(lanes + kColU + 32 * kh + 16 * part, u);
-                if (has_m) tmem_ld16(lanes + kColF + 32 * kh + 16 * part, f);
+            float u[32];
+            tmem_ld32(lanes + kColU + 32 * kh, u);
+            if (has_m) {
+                float f[32];
+                tmem_ld32(lanes + kColF + 32 * kh, f);
                 tmem_ld_wait();
-                uint32_t p[8];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) {
-                    float a = S.scale * u[2 * x], b = S.scale * u[2 * x + 1];
-                    if (has_m) {
-                        a = fmaf(bi, f[2 * x], a);
-                        b = fmaf(bi, f[2 * x + 1], b);
-                    }
-                    p[x] = pack_bf16x2(a, b);
-                }
-                if (copied) {
+                for (int x = 0; x < 32; ++x) u[x] = fmaf(bi, f[x], S.scale * u[x]);
+            } else {
+                tmem_ld_wait();
 #pragma unroll
-                    for (int x = 0; x < 2; ++x)
-                        sts128(o + kmajor_chunk(row, 4 * kh + 2 * part + x), p[4 * x], p[4 * x + 1],
-                               p[4 * x + 2], p[4 * x + 3]);
-                } else if (row < n) {
-                    uint4* g = reinterpret_cast<uint4*>(I.out + row * kD + 32 * kh + 16 * part);
-                    g[0] = make_uint4(p[0], p[1], p[2], p[3]);
-                    g[1] = make_uint4(p[4], p[5], p[6], p[7]);
-                }
+                for (int x = 0; x < 32; ++x) u[x] *= S.scale;
             }
             tc_fence_before();
             warp_arrive(&ctl.out_free);
-            if (copied) {
-                fence_proxy_async();
-                named_bar_sync(1 + qw, 64);
-                if (lane == 0 && kh == 0 && 32 * qw < n) {
-                    tma_store_3d(I.o, sm + kMOffO + qw * 32 * 128, 0, I.t0 + 32 * qw, I.plane);
-                    bulk_commit();
+            if (row < n) {
+                const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t p[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        p[x] = pack_bf16x2(u[16 * half + 2 * x], u[16 * half + 2 * x + 1]);
+                    store16(out + 16 * half, p, wide);
                 }
             }
-            warp_arrive(&ctl.info_free[done & 1]);
+            warp_arrive(&ctl.info_free[done % kInfos]);
         }
-        if (lane == 0 && kh == 0) bulk_wait0();
     } else if (warp == kAheadWarp) {
-        bool ok = true;
-        for (int idx = blockIdx.x, done = 0; ok; idx += gridDim.x) {
+        int nx = 0, nm = 0, nyz = 0, done = 0;
+        bool ok = true, waited = false;
+        for (int idx = blockIdx.x;; idx += gridDim.x, ++done) {
             MixItem it;
             it.n = 0;
             for (; idx < items; idx += gridDim.x)
                 if ((it = mix_item(jobs, S, idx)).n > 0) break;
-            if (done >= 2) ok = wait_all(&ctl.info_free[done & 1], ((done >> 1) - 1) & 1, abort_flag);
+            if (done >= kInfos)
+                ok = wait_all_sleep(&ctl.info_free[done % kInfos], (done / kInfos - 1) & 1, abort_flag);
             if (!ok) break;
-            MixInfo& I = infos[done & 1];
-            if (idx < items) {
-                const MixJob& J = jobs.job[it.w];
+            MixInfo& I = infos[done % kInfos];
+            const bool none = idx >= items;
+            const MixJob& J = jobs.job[it.n > 0 ? it.w : 0];
+            if (!none) {
                 const float g = decay_log(S.log_decay, it.kv);
-                for (int i = lane; i <= kC; i += 32) I.pw[1 + i] = decay_pow(g, i);
+                I.pw[1 + lane] = 0.f;
+                #pragma unroll
+                for (int i = 0; i < kC; i += 32) I.pw[kPw0 + i + lane] = decay_pow(g, i + lane);
+                if (lane == 0) I.pw[kPw0 + kC] = decay_pow(g, kC);
                 if (lane == 0) {
                     const int left = S.T - it.c * kC, plane = it.b * J.j.hx + it.hx;
                     I.out = static_cast<__nv_bfloat16*>(J.j.out) +
                             (size_t(plane) * S.T + it.c * kC) * kD;
-                    I.o = it.n == min(kC, left) ? &J.o : nullptr;
                     I.n = it.n;
                     I.nh = it.nh;
                     I.rev = J.j.rev;
                     I.has_m = it.has_m;
-                    I.t0 = it.c * kC;
-                    I.plane = plane;
+                    I.mem_t = J.j.mem_t;
                     I.garbage = it.n < kC && it.n < left;
                 }
             }
-            if (lane == 0) I.none = idx >= items;
-            warp_arrive(&ctl.info_full[done & 1]);
-            ++done;
-            if (idx >= items) break;
+            if (lane == 0) I.none = none;
+            warp_arrive(&ctl.info_full[done % kInfos]);
+            if (none) break;
+            if (lane == 0) {
+                // Y and Z of a step go where those of two steps before were, once P Z has read them
+                // (a barrier of each stage: this warp may lag behind pv_done by two phases, which
+                // a parity cannot tell from none)
+                auto load_yz = [&](int h) {
+                    if (nyz >= 2)
+                        ok = mbar_wait_sleep(&ctl.yz_free[nyz & 1], ((nyz >> 1) - 1) & 1, abort_flag);
+                    if (!ok) return;
+                    unsigned char* dst = sm + kMOffYZ + (nyz & 1) * 2 * kTile;
+                    uint64_t* bar = &ctl.yz_full[nyz & 1];
+                    const int plane = it.b * J.j.hy + it.y0 + h;
+                    mbar_expect_tx(bar, 2 * kTile);
+                    tma_load_3d(dst, &J.y, bar, 0, it.c * kC, plane);
+                    tma_load_3d(dst + kTile, &J.z, bar, 0, it.c * kC, plane);
+                    ++nyz;
+                };
+                if (done > 0) ok = mbar_wait_sleep(&ctl.x_free, (done - 1) & 1, abort_flag);
+                if (ok) {
+                    mbar_expect_tx(&ctl.x_full, kTile);
+                    tma_load_3d(sm + kMOffX, &J.x, &ctl.x_full, 0, it.c * kC, it.b * J.j.hx + it.hx);
+                    ++nx;
+                    load_yz(0);
+                }
+                // (the inputs were there before the kernels whose results this one waits for)
+                if (!waited) grid_dep_wait();
+                waited = true;
+                if (ok && it.has_m) {
+                    mbar_expect_tx(&ctl.m_full, kMTile);
+                    tma_load_2d(sm + kMOffM, &J.m, &ctl.m_full, 0,
+                                ((it.b * S.Hkv + it.kv) * S.chunks + it.c) * 64);
+                    ++nm;
+                }
+                for (int h = 1; ok && h < it.nh; ++h) load_yz(h);
+            }
+            ok = __shfl_sync(~0u, ok ? 1 : 0, 0) != 0;
+            if (!ok) break;
+        }
+        if (lane == 0) {
+            if (!waited) grid_dep_wait();
+            // no copy is in flight when the CTA ends
+            if (nx) bounded_spin_done(&ctl.x_full, (nx - 1) & 1);
+            if (nm) bounded_spin_done(&ctl.m_full, (nm - 1) & 1);
+            if (nyz) bounded_spin_done(&ctl.yz_full[(nyz - 1) & 1], ((nyz - 1) >> 1) & 1);
+            if (nyz > 1) bounded_spin_done(&ctl.yz_full[nyz & 1], ((nyz - 2) >> 1) & 1);
         }
     } else if (lane == 0) {
         constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
         constexpr uint32_t id_mn = idesc_bf16(128, 64, false, true), id_k = idesc_bf16(128, 64, false, false);
         const uint32_t x = smem_u32(sm + kMOffX), m = smem_u32(sm + kMOffM);
         const uint32_t yz = smem_u32(sm + kMOffYZ);
-        int nx = 0, nm = 0, nyz = 0, npv = 0, nfree = 0;
-        auto load_x = [&](const MixItem& it) {
-            const MixJob& J = jobs.job[it.w];
-            mbar_expect_tx(&ctl.x_full, kTile);
-            tma_load_3d(sm + kMOffX, &J.x, &ctl.x_full, 0, it.c * kC, it.b * J.j.hx + it.hx);
-            ++nx;
-        };
-        auto load_m = [&](const MixItem& it) {
-            if (!it.has_m) return;
-            mbar_expect_tx(&ctl.m_full, kMTile);
-            tma_load_2d(sm + kMOffM, &jobs.job[it.w].m, &ctl.m_full, 0,
-                        ((it.b * S.Hkv + it.kv) * S.chunks + it.c) * 64);
-            ++nm;
-        };
-        auto load_yz = [&](const MixItem& it, int h) {
-            unsigned char* dst = sm + kMOffYZ + (nyz & 1) * 2 * kTile;
-            uint64_t* bar = &ctl.yz_full[nyz & 1];
-            const MixJob& J = jobs.job[it.w];
-            const int plane = it.b * J.j.hy + it.y0 + h;
-            mbar_expect_tx(bar, 2 * kTile);
-            tma_load_3d(dst, &J.y, bar, 0, it.c * kC, plane);
-            tma_load_3d(dst + kTile, &J.z, bar, 0, it.c * kC, plane);
-            ++nyz;
-        };
-        auto next = [&](int& idx, MixItem& it) {
-            for (; idx < items; idx += gridDim.x)
-                if ((it = mix_item(jobs, S, idx)).n > 0) return true;
-            return false;
-        };
-        int idx = blockIdx.x, step = 0, used_m = 0;
-        MixItem it, nit;
-        bool more = next(idx, it), ok = true;
-        // the inputs were there before the kernels whose results this one waits for
-        if (more) {
-            load_x(it);
-            load_yz(it, 0);
-        }
-        grid_dep_wait();
-        if (more) load_m(it);
-        for (int done = 0; more && ok; ++done) {
-            int nidx = idx;
-            bool nmore = false;
+        int nm = 0, npv = 0, nfree = 0, step = 0;
+        bool ok = true;
+        for (int done = 0; ok; ++done) {
+            ok = mbar_wait(&ctl.info_full[done % kInfos], (done / kInfos) & 1, abort_flag);
+            const MixInfo& I = infos[done % kInfos];
+            if (!ok || I.none) break;
+            const int nh = I.nh, has_m = I.has_m, mem_t = I.mem_t;
             ok = mbar_wait(&ctl.x_full, done & 1, abort_flag);
-            for (int h = 0; h < it.nh && ok; ++h, ++step) {
-                const bool last = h == it.nh - 1;
-                ok = mbar_wait(&ctl.yz_full[step & 1], (step >> 1) & 1, abort_flag);
+            for (int h = 0; ok && h < nh; ++h, ++step) {
+                ok = mbar_wait(&ctl.yz_full[step & 1], (step >> 1) & 1, abort_flag) &&
+                     // the scores go over P of the step before
+                     (step == 0 || mbar_wait(&ctl.pv_done, (step - 1) & 1, abort_flag));
                 if (!ok) break;
                 const uint32_t y = yz + (step & 1) * 2 * kTile, z = y + kTile;
                 tc_fence_after();
@@ -594,30 +607,25 @@ __global__ void __launch_bounds__(kMixThreads, 2)
                     mma_bf16(tmem + kColS, sdesc_sw128(x + ks * 32, 16, 1024),
                              sdesc_sw128(y + ks * 32, 16, 1024), id_s, ks > 0 ? 1u : 0u);
                 mma_commit(&ctl.s_full);
-                if (h == 0) nmore = next(nidx += gridDim.x, nit);  // while the scores are formed
-                // the other stage is free: the products that read it are done
-                if (!last) load_yz(it, h + 1);
-                else if (nmore) load_yz(nit, 0);
                 if (h == 0) {
                     // U and F of the item before have been read
                     if (done > 0) ok = mbar_wait(&ctl.out_free, (done - 1) & 1, abort_flag);
-                    if (ok && it.has_m) {
-                        ok = mbar_wait(&ctl.m_full, used_m & 1, abort_flag);
-                        ++used_m;
+                    if (ok && has_m) {
+                        ok = mbar_wait(&ctl.m_full, nm & 1, abort_flag);
+                        ++nm;
                         if (ok) {
                             tc_fence_after();
-                            const bool t = jobs.job[it.w].j.mem_t;
 #pragma unroll
                             for (int ks = 0; ks < 4; ++ks)
                                 mma_bf16(tmem + kColF, sdesc_sw128(x + ks * 32, 16, 1024),
-                                         t ? sdesc_sw128(m + ks * 32, 16, 1024)
-                                           : sdesc_sw128(m + ks * 2048, kTile, 1024),
-                                         t ? id_k : id_mn, ks > 0 ? 1u : 0u);
+                                         mem_t ? sdesc_sw128(m + ks * 32, 16, 1024)
+                                               : sdesc_sw128(m + ks * 2048, kTile, 1024),
+                                         mem_t ? id_k : id_mn, ks > 0 ? 1u : 0u);
                         }
                     }
                     if (!ok) break;
                 }
-                if (last) {
+                if (h == nh - 1) {
                     mma_commit(&ctl.x_free);  // no later MMA of the item reads X or M
                     ++nfree;
                 }
@@ -626,36 +634,22 @@ __global__ void __launch_bounds__(kMixThreads, 2)
                 tc_fence_after();
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                    mma_bf16_ts(tmem + kColU, tmem + kColS + (ks < 4 ? 8 * ks : 64 + 8 * (ks - 4)),
+                    mma_bf16_ts(tmem + kColU, tmem + kColS + 32 * (ks >> 1) + 8 * (ks & 1),
                                 sdesc_sw128(z + ks * 2048, kTile, 1024), id_mn,
                                 (h > 0 || ks > 0) ? 1u : 0u);
                 mma_commit(&ctl.pv_done);
+                mma_commit(&ctl.yz_free[step & 1]);
                 ++npv;
-                if (last && nmore) {
-                    ok = mbar_wait(&ctl.x_free, done & 1, abort_flag);
-                    if (!ok) break;
-                    load_x(nit);
-                    load_m(nit);
-                }
-                // the next scores go over P, and the next loads over this step's Y and Z
-                ok = mbar_wait(&ctl.pv_done, step & 1, abort_flag);
             }
-            idx = nidx;
-            it = nit;
-            more = nmore;
         }
-        // nothing of this CTA is in flight when it ends
-        if (nx) bounded_spin_done(&ctl.x_full, (nx - 1) & 1);
-        if (nm) bounded_spin_done(&ctl.m_full, (nm - 1) & 1);
-        if (nyz) bounded_spin_done(&ctl.yz_full[(nyz - 1) & 1], ((nyz - 1) >> 1) & 1);
-        if (nyz > 1) bounded_spin_done(&ctl.yz_full[nyz & 1], ((nyz - 2) >> 1) & 1);
+        // every MMA has completed before tensor memory is freed
         if (nfree) bounded_spin_done(&ctl.x_free, (nfree - 1) & 1);
-        if (npv) bounded_spin_done(&ctl.pv_done, (npv - 1) & 1);
+        if (npv) bounded_spin_done(&ctl.yz_free[(npv - 1) & 1], ((npv - 1) >> 1) & 1);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == kCtrlWarp) {
+    if (warp == kMmaWarp) {
         tc_fence_after();
         tmem_dealloc(tmem, kMixTmem);
     }

@@ -57,6 +57,8 @@ _VP, _SZ, _PS = ctypes.c_void_p, ctypes.c_size_t, ctypes.POINTER(Shape)
 def lib() -> ctypes.CDLL:
     """The loaded liboal.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -602,15 +604,25 @@ def backward_workspace(q, k, v) -> torch.Tensor:
     return empty_workspace(n.value, q.device)
 
 
-class _on:
-    """The device and stream of a call: tensors made inside belong to that stream, so that their
-    memory is not handed out again before the call's kernels are done with it.  Where the stream
-    is the device's current one already, nothing is switched."""
+class _Here:
+    """A call on the current device and its current stream: nothing to switch."""
+    __slots__ = ("stream",)
+
+    def __init__(self, stream):
+        self.stream = stream
+
+    def __enter__(self):
+        return self.stream
+
+    def __exit__(self, *exc):
+        pass
+
+
+class _There:
+    """A call on another device or stream, which are current inside."""
 
     def __init__(self, device, stream):
-        self.ctx = []
-        if device.index is not None and device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(device))
+        self.ctx = [torch.cuda.device(device)]
         if stream is not None:
             self.ctx.append(torch.cuda.stream(stream))
 
@@ -624,6 +636,16 @@ class _on:
             c.__exit__(*exc)
 
 
+def _on(device, stream):
+    """The device and stream of a call, as a context that gives the stream's handle.  Tensors made
+    inside belong to that stream, so that their memory is not handed out again before the call's
+    kernels are done with it."""
+    index = device.index
+    if stream is None and index == torch._C._cuda_getDevice():
+        return _Here(torch._C._cuda_getCurrentRawStream(index))
+    return _There(device, stream)
+
+
 def _need(name, t, shape, dtype, device, optional=False):
     """Refuses a tensor that is not a contiguous CUDA tensor of this shape, type and device."""
     if t is None:
@@ -634,7 +656,7 @@ def _need(name, t, shape, dtype, device, optional=False):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device or not t.is_cuda or not t.is_contiguous():
+    if not t.is_cuda or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
     return t.data_ptr()
 
@@ -835,7 +857,8 @@ def _state_of(name, t, B, Hq, Hkv, dev):
         raise TypeError(f"{name} must be a state buffer (uint8, one dimension)")
     if t.device != dev or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
-    empty = state_bytes(Shape(0, 1, Hq, Hkv, 64, 64, 128, OAL_BF16))
+    # the layout of oal_state_bytes: header and coefficient tables, then the sequences
+    empty = 256 + (Hq * FEATURES_PAD * 4 + 255) // 256 * 256
     one = Hkv * FEATURES_PAD * (VALUE_DIM + 1) * 4
     held = (t.numel() - empty) // one
     if t.numel() < empty or (B is not None and held < B):
