@@ -411,6 +411,20 @@ cudaError_t set_attributes_once()
     return cudaSuccess;
 }
 
+// [heads][T][64] bf16 for copies out of 32 rows by 32 columns (what a warp has)
+bool make_out_map(CUtensorMap* m, const void* base, int T, int heads)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {64, cuuint64_t(T), cuuint64_t(heads)};
+    const cuuint64_t strides[2] = {64 * 2, cuuint64_t(T) * 64 * 2};
+    const cuuint32_t box[3] = {32, 32, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // [planes][64] bf16 state images of 64 rows each, as 2D {64, planes * 64}
 bool make_state_map(CUtensorMap* m, const void* base, size_t planes)
 {
@@ -475,16 +489,16 @@ int launch_mix(const DecayShape& S, const DecayJob* j, const DecaySum* const* su
         dtc::MixJob& m = jobs.job[i];
         m.j = j[i];
         m.has_first = sums[i]->first != nullptr;
-        m.items = s->B * j[i].hx * S.chunks;
-        items += m.items;
+        items += (long long)s->B * j[i].hx * S.chunks;
         if (!make_map_uncached(&m.x, j[i].x, s->T, s->B * j[i].hx) ||
             !make_map_uncached(&m.y, j[i].y, s->T, s->B * j[i].hy) ||
             !make_map_uncached(&m.z, j[i].z, s->T, s->B * j[i].hy) ||
+            !make_out_map(&m.o, j[i].out, s->T, s->B * j[i].hx) ||
             !make_state_map(&m.m, j[i].mem, size_t(s->B) * s->Hkv * S.chunks))
             return OAL_ERR_CUDA;
     }
     OAL_CUDA_TRY(launch_ex(dtc::mix_kernel, dim3(int(std::min<long long>(items, 2 * sm_count()))),
-                           dim3(dtc::kMixThreads), dtc::kMixSmem, st, true, jobs, S, int(items)));
+                           dim3(dtc::kMixThreads), dtc::kMixSmem, st, true, jobs, S));
     return OAL_OK;
 }
 

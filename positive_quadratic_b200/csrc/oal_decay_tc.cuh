@@ -20,6 +20,32 @@ constexpr int kCtrlWarp = 8;
 constexpr uint32_t kTile = kC * 128;      // a 128 x 64 bf16 tile
 constexpr uint32_t kMTile = 64 * 128;     // a 64 x 64 bf16 state image
 
+// tc::mbar_wait with its time limit taken from the SM's clock: a wait costs two or three
+// instructions per poll.  (Reading the global timer takes about a thousand cycles, which every
+// wait that does not succeed at once would pay before it looks again.)
+constexpr long long kWaitLimitCycles = 2000000000ll;  // 1 s at 1.965 GHz
+
+__device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (clock64() - t0 > kWaitLimitCycles) {
+            *abort_flag = 1;
+            raise_error(OAL_ERR_TIMEOUT);
+            return false;
+        }
+    }
+}
+
+// The same by a whole warp.
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag)
+{
+    return __all_sync(~0u, wait(bar, parity, abort_flag));
+}
+
 // 32 lanes x 32 consecutive 32-bit columns (see tmem_ld16).
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
 {
@@ -131,9 +157,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t lo = smem_u32(sm + kDOffLo);
             bool ok = true;
             for (int i = 0; i < nh; ++i) {
-                ok = wait_all(&ctl.y_full, i & 1, abort_flag) &&
-                     wait_all(&ctl.z_full[i & 1], (i >> 1) & 1, abort_flag) &&
-                     (i == 0 || wait_all(&ctl.done, (i - 1) & 1, abort_flag));
+                ok = wait_warp(&ctl.y_full, i & 1, abort_flag) &&
+                     wait_warp(&ctl.z_full[i & 1], (i >> 1) & 1, abort_flag) &&
+                     (i == 0 || wait_warp(&ctl.done, (i - 1) & 1, abort_flag));
                 if (!ok) break;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -160,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 fence_proxy_async();
                 warp_arrive(&ctl.parts);
             }
-            ok = ok && wait_all(&ctl.done, (nh - 1) & 1, abort_flag);
+            ok = ok && wait_warp(&ctl.done, (nh - 1) & 1, abort_flag);
             ok = named_bar_and(1, 256, ok);
             if (ok) {
                 tc_fence_after();
@@ -221,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             load_z(0);
             if (nh > 1) load_z(1);
             for (int i = 0; i < nh; ++i) {
-                if (!mbar_wait(&ctl.parts, i & 1, abort_flag)) break;
+                if (!wait(&ctl.parts, i & 1, abort_flag)) break;
                 if (i + 1 < nh) load_y(i + 1);  // the parts of head i have been formed
                 tc_fence_after();
                 const uint32_t zi = z + (i & 1) * kTile;
@@ -236,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 mma_commit(&ctl.done);
                 ++nmma;
                 if (i + 2 < nh) {
-                    if (!mbar_wait(&ctl.done, i & 1, abort_flag)) break;
+                    if (!wait(&ctl.done, i & 1, abort_flag)) break;
                     load_z(i + 2);
                 }
             }
@@ -261,7 +287,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 //   S_h = X Y_h^T (tensor memory), P_h = bf16(S_h o D) written over it, U = sum_h P_h Z_h,
 //   F = X M (the bf16 state before the chunk), out = scale U + b F.
 // The decay of the far part is applied to F's rows in fp32, so that q and S are rounded once.
-// Persistent: two CTAs per SM, each walking items blockIdx.x, blockIdx.x + gridDim.x, ...
+// Persistent: two CTAs per SM, each with a run of neighbouring items of about equal work.  The
+// items of a job are ordered (b, chunk, kv, head of the group): query heads that share keys,
+// values and a state follow one another, and Y, Z and M stay where they are for them.
 // Warps 0-7 compute: warp (qw, kh) holds rows 32 qw .. + 31 (its tensor-memory lanes), keys
 // 64 kh .. + 63 of the scores and columns 32 kh .. + 31 of the output.  Warp 8 issues the MMAs;
 // the next item's scores are formed while the compute warps write out the present one's result.
@@ -269,10 +297,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 // as soon as buffers are free.
 // ------------------------------------------------------------------------------------------
 struct MixJob {
-    CUtensorMap x, y, z, m;
+    CUtensorMap x, y, z, m, o;
     DecayJob j;
     int has_first;  // the chunk at the start of the scan has a state, too
-    int items;      // of this job
 };
 struct MixJobs {
     MixJob job[3];
@@ -284,23 +311,33 @@ constexpr int kMixThreads = (kMixWarps + 2) * 32;
 constexpr int kMmaWarp = kMixWarps, kAheadWarp = kMixWarps + 1;
 constexpr int kInfos = 4;  // items that the look-ahead warp may have described and not seen done
 
-// What the other warps need to know of an item, and the powers of l: l^i at pw[kPw0 + i], so that
-// pairs that start at an odd power are 8-byte aligned and 31 places lie before the first.
+// What the other warps need to know of an item, and the powers of l in either order, so that a row's
+// factors are read in the order of its keys: l^i at up[kPw0 + i], l^(127 - i) at down[kPw0 + i].  Pairs
+// that start at an odd place are 8-byte aligned; the factors of a diagonal block's other side lie up
+// to 31 places before the first power (up) or behind the last (down) and are not used.
 constexpr int kPw0 = 33;
 struct MixInfo {
-    __nv_bfloat16* out;  // the tile's first row
-    int n, nh, rev, has_m, mem_t, garbage, none, pad;
-    float pw[kPw0 + kC + 3];
+    __nv_bfloat16* out;    // the tile's first row
+    const CUtensorMap* o;  // of the output; NULL: rows behind the sequence's end are not to be written
+    int n, nh, rev, has_m, mem_t, t0, plane, garbage, none;
+    int fresh, last;  // first, last item of a run that shares Y, Z and M
+    int pad;
+    float up[kPw0 + kC + 1], down[kPw0 + kC + 31];
 };
 
 struct MixCtl {
-    uint64_t x_full, m_full, yz_full[2], yz_free[2], s_full, p_full, pv_done, x_free, out_free;
-    uint64_t info_full[kInfos], info_free[kInfos];
+    uint64_t x_full[2];            // an item's X has arrived (and its description, before)
+    uint64_t x_free[2];            // its output has left the buffer, where it is staged
+    uint64_t yz_full[2], m_full;
+    uint64_t s_full, p_full;       // of a step
+    uint64_t yz_free[2], m_free;   // the products that read them are done
+    uint64_t item_done[2];         // every product of the item is done
+    uint64_t info_full[kInfos], info_free[kInfos], drained;
     uint32_t tmem_base;
     int abort_flag;
 };
 
-constexpr uint32_t kMOffX = 0, kMOffYZ = kTile, kMOffM = 5 * kTile;
+constexpr uint32_t kMOffX = 0, kMOffYZ = 2 * kTile, kMOffM = 6 * kTile;
 constexpr uint32_t kMOffInfo = kMOffM + kMTile;
 constexpr uint32_t kMOffCtl = kMOffInfo + kInfos * sizeof(MixInfo);
 constexpr uint32_t kMixSmem = kMOffCtl + 256 + 1024;
@@ -308,100 +345,177 @@ constexpr uint32_t kMixTmem = 256;
 constexpr uint32_t kColS = 0, kColU = 128, kColF = 192;
 static_assert(sizeof(MixCtl) <= 256 && kMOffCtl % 8 == 0 && 2 * (kMixSmem + 1024) <= 233472,
               "two CTAs per SM");
-static_assert(sizeof(MixInfo) % 8 == 0 && offsetof(MixInfo, pw) % 8 == 0 && kPw0 % 2 == 1, "alignment of pw");
+static_assert(sizeof(MixInfo) % 8 == 0 && offsetof(MixInfo, up) % 8 == 0 &&
+                  offsetof(MixInfo, down) % 8 == 0 && kPw0 % 2 == 1,
+              "alignment of the powers");
+static_assert(kMixWarps * 2048 <= kTile, "output staging");
 
-struct MixItem {
-    int w, b, hx, kv, c, n, nh, y0, has_m;
+// A CTA's place in the work: item `i` of job w, at (b, chunk c, kv, head gi of the group).  Held by
+// the look-ahead warp, whose lanes all carry the same values.
+struct MixWalk {
+    int w, i, items, b, c, kv, gi, len, n;
+    long long left;  // work units of this CTA from the present item on
+
+    __device__ __forceinline__ static int chunks_of(const DecayShape& S, int b)
+    {
+        return (decay_len(S, b) + kC - 1) / kC;
+    }
+    // chunks of all sequences
+    __device__ __forceinline__ static int live_chunks(const DecayShape& S, int lane)
+    {
+        if (!S.lens) return S.B * S.chunks;
+        int sum = 0;
+        for (int b = lane; b < S.B; b += 32) sum += chunks_of(S, b);
+        return __reduce_add_sync(~0u, sum);
+    }
+    // the place of the q-th chunk
+    __device__ __forceinline__ void at_chunk(const DecayShape& S, int q, int lane)
+    {
+        if (!S.lens) {
+            b = q / S.chunks;
+            c = q % S.chunks;
+        } else {
+            b = 0;
+            while (true) {  // 32 sequences at a time
+                const int mine = b + lane < S.B ? chunks_of(S, b + lane) : 0;
+                int upto = mine;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(~0u, upto, o);
+                    if (lane >= o) upto += x;
+                }
+                const uint32_t hit = __ballot_sync(~0u, upto > q);
+                if (hit || b + 32 >= S.B) {
+                    const int l = hit ? __ffs(hit) - 1 : 31;
+                    c = q - __shfl_sync(~0u, upto - mine, l);
+                    b += l;
+                    break;
+                }
+                q -= __shfl_sync(~0u, upto, 31);
+                b += 32;
+            }
+        }
+        len = decay_len(S, b);
+    }
+    __device__ __forceinline__ static int heads(const DecayJob& j, int Hkv) { return j.hx / Hkv; }
+    __device__ __forceinline__ static int steps(const DecayJob& j)
+    {
+        return j.hy > j.hx ? j.hy / j.hx : 1;
+    }
+    __device__ __forceinline__ void place(const MixJobs& jobs, const DecayShape& S, int lane)
+    {
+        const int grp = heads(jobs.job[w].j, S.Hkv);
+        gi = i % grp;
+        kv = i / grp % S.Hkv;
+        at_chunk(S, i / grp / S.Hkv, lane);
+    }
+    // This CTA's share: the items that start within [total k / grid, total (k + 1) / grid).
+    __device__ __forceinline__ void start(const MixJobs& jobs, const DecayShape& S, int lane)
+    {
+        const long long rows = (long long)live_chunks(S, lane) * S.Hkv;
+        long long total = 0;
+        for (int k = 0; k < jobs.n; ++k)
+            total += rows * heads(jobs.job[k].j, S.Hkv) * steps(jobs.job[k].j);
+        long long lo = total * blockIdx.x / gridDim.x;
+        left = total * (blockIdx.x + 1) / gridDim.x - lo;
+        for (w = 0;; ++w) {
+            const int st = steps(jobs.job[w].j);
+            items = int(rows * heads(jobs.job[w].j, S.Hkv));
+            const long long first = (lo + st - 1) / st;
+            if (first < items || w + 1 == jobs.n) {
+                i = int(min(first, (long long)items));
+                left -= first * st - lo;
+                break;
+            }
+            // the next job's first item may start later than lo
+            const long long over = (long long)items * st - lo;
+            left -= max(over, 0ll);
+            lo = max(-over, 0ll);
+        }
+        if (more()) place(jobs, S, lane);
+    }
+    __device__ __forceinline__ bool more() const { return left > 0 && i < items; }
+    // To the next item; whether there is one.
+    __device__ __forceinline__ void advance(const MixJobs& jobs, const DecayShape& S, int lane)
+    {
+        left -= steps(jobs.job[w].j);
+        if (++i == items) {
+            if (w + 1 == jobs.n) return;
+            const int rows = items / heads(jobs.job[w].j, S.Hkv);
+            ++w;
+            i = 0;
+            items = rows * heads(jobs.job[w].j, S.Hkv);
+            if (more()) place(jobs, S, lane);
+            return;
+        }
+        if (++gi < heads(jobs.job[w].j, S.Hkv)) return;
+        gi = 0;
+        if (++kv < S.Hkv) return;
+        kv = 0;
+        if (++c * kC < len) return;
+        c = 0;
+        do
+            len = ++b < S.B ? decay_len(S, b) : 1;
+        while (len == 0);
+    }
 };
 
-// Item `idx`; n <= 0 if it has no tokens.  Items of a job: (b, kv, chunk, head of the group), so
-// that the heads that share keys, values and a state run side by side.
-__device__ __forceinline__ MixItem mix_item(const MixJobs& jobs, const DecayShape& S, int idx)
-{
-    MixItem it;
-    it.w = 0;
-    while (it.w + 1 < jobs.n && idx >= jobs.job[it.w].items) idx -= jobs.job[it.w++].items;
-    const DecayJob& j = jobs.job[it.w].j;
-    const int grpx = j.hx / S.Hkv;
-    const int gi = idx % grpx, r = idx / grpx;
-    it.c = r % S.chunks;
-    it.kv = (r / S.chunks) % S.Hkv;
-    it.b = r / S.chunks / S.Hkv;
-    it.hx = it.kv * grpx + gi;
-    it.nh = j.hy > j.hx ? j.hy / j.hx : 1;
-    it.y0 = j.hy > j.hx ? it.hx * it.nh : it.kv * (j.hy / S.Hkv) + (j.hy == j.hx ? gi : 0);
-    const int len = decay_len(S, it.b);
-    it.n = min(kC, len - it.c * kC);
-    it.has_m = it.c != (j.rev ? (len - 1) / kC : 0) || jobs.job[it.w].has_first;
-    return it;
-}
-
 // P = S o D for rows 32 qw + lane and keys 32 jb .. + 31, written over the scores.
-template <bool kRev>
-__device__ __forceinline__ void decay_scores(uint32_t scores, const float* pw, int qw, int jb,
-                                             int lane, int n)
+__device__ __forceinline__ void decay_scores(uint32_t scores, const MixInfo& I, int qw, int jb,
+                                             int lane)
 {
+    const int rev = I.rev, left = I.n - 32 * jb;
+    // keys that count: this side of the diagonal, and not behind the sequence's end (which matters
+    // where rows look at later keys)
+    const uint32_t before = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1;
+    uint32_t live = rev ? before : ~0u;
+    const int ahead = rev ? jb - qw : qw - jb;  // blocks between the rows and the keys
+    if (ahead == 0) live &= rev ? ~0u << lane : ~0u >> (31 - lane);
     uint32_t p[16];
-    if (jb == qw) {  // the diagonal block
-        float s[32];
-        tmem_ld32(scores, s);
-        tmem_ld_wait();
-#pragma unroll
-        for (int x = 0; x < 32; ++x) {
-            // on the wrong side of the diagonal the factor is whatever lies there, and the
-            // product (which may be NaN, as may what lies behind the end) is not taken
-            const float d = kRev ? pw[kPw0 + x - lane] : pw[kPw0 + lane - x];
-            const float v = s[x] * d;
-            s[x] = (kRev ? x >= lane && 32 * jb + x < n : x <= lane) ? v : 0.f;
-        }
-#pragma unroll
-        for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(s[2 * x], s[2 * x + 1]);
-    } else if (kRev ? jb > qw : jb < qw) {
-        // l^|i-j| = l^(from the row to its block's edge) l^(from there to j)
-        float s[32];
-        tmem_ld32(scores, s);
-        const float rf = pw[kPw0 + (kRev ? 31 - lane : lane)];
-        const float2 rf2 = make_float2(rf, rf);
-        // the pair of columns (x, x + 1): powers at + x and at + x + 1 (kRev), or - x, - x - 1
-        const float* at = pw + kPw0 + (kRev ? 32 * (jb - qw) - 31 : 32 * (qw - jb) - 1);
-        tmem_ld_wait();
-#pragma unroll
-        for (int x = 0; x < 32; x += 2) {
-            float2 d = *reinterpret_cast<const float2*>(kRev ? at + x : at - x);
-            if (!kRev) d = make_float2(d.y, d.x);
-            const float2 v = __fmul2_rn(make_float2(s[x], s[x + 1]), __fmul2_rn(rf2, d));
-            s[x] = v.x;
-            s[x + 1] = v.y;
-        }
-        if (kRev && n < kC)  // keys behind the sequence's end, whatever they gave
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-                if (32 * jb + x >= n) s[x] = 0.f;
-#pragma unroll
-        for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(s[2 * x], s[2 * x + 1]);
-    } else {
+    if (ahead < 0) {
 #pragma unroll
         for (int x = 0; x < 16; ++x) p[x] = 0u;
+    } else {
+        float s[32];
+        tmem_ld32(scores, s);
+        if (ahead == 0) {
+            const float* d = rev ? I.up + kPw0 - lane : I.down + kPw0 + 127 - lane;
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) s[x] *= d[x];
+        } else {
+            // l^|i-j| = l^(from the row to its block's edge) l^(from there to j)
+            const float rf = I.up[kPw0 + (rev ? 31 - lane : lane)];
+            const float* d = rev ? I.up + kPw0 + 32 * ahead - 31 : I.down + kPw0 + 127 - 32 * ahead;
+            const float2 rf2 = make_float2(rf, rf);
+            tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+                const float2 v = __fmul2_rn(make_float2(s[x], s[x + 1]),
+                                            __fmul2_rn(rf2, *reinterpret_cast<const float2*>(d + x)));
+                s[x] = v.x;
+                s[x + 1] = v.y;
+            }
+        }
+        if (__any_sync(~0u, live != ~0u)) {
+            // chosen, not multiplied by zero: what is not live may be NaN
+#pragma unroll
+            for (int x = 0; x < 32; ++x) s[x] = (live >> x) & 1 ? s[x] : 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(s[2 * x], s[2 * x + 1]);
     }
     tmem_st16(scores, p);
 }
 
-// Stores 16 bf16 values (32 bytes; one store where the address allows it).
-__device__ __forceinline__ void store16(__nv_bfloat16* out, const uint32_t (&p)[8], bool wide)
+__device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, int x, int y, int z)
 {
-    if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out),
-                     "r"(p[0]), "r"(p[1]), "r"(p[2]), "r"(p[3]), "r"(p[4]), "r"(p[5]), "r"(p[6]),
-                     "r"(p[7])
-                     : "memory");
-    } else {
-        reinterpret_cast<uint4*>(out)[0] = make_uint4(p[0], p[1], p[2], p[3]);
-        reinterpret_cast<uint4*>(out)[1] = make_uint4(p[4], p[5], p[6], p[7]);
-    }
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];"
+                 ::"l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+                 : "memory");
 }
 
 __global__ void __launch_bounds__(kMixThreads, 2)
-    mix_kernel(const __grid_constant__ MixJobs jobs, DecayShape S, int items)
+    mix_kernel(const __grid_constant__ MixJobs jobs, DecayShape S)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char* sm = smem_raw + (-smem_u32(smem_raw) & 1023u);  // still known to be shared
@@ -411,17 +525,18 @@ __global__ void __launch_bounds__(kMixThreads, 2)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
-        mbar_init(&ctl.x_full, 1);
         mbar_init(&ctl.m_full, 1);
+        mbar_init(&ctl.m_free, 1);
+        mbar_init(&ctl.drained, 1);
         mbar_init(&ctl.s_full, 1);
         mbar_init(&ctl.p_full, kMixWarps);
-        mbar_init(&ctl.pv_done, 1);
-        mbar_init(&ctl.x_free, 1);
-        mbar_init(&ctl.out_free, kMixWarps);
-        mbar_init(&ctl.yz_full[0], 1);
-        mbar_init(&ctl.yz_full[1], 1);
-        mbar_init(&ctl.yz_free[0], 1);
-        mbar_init(&ctl.yz_free[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.x_full[i], 1);
+            mbar_init(&ctl.item_done[i], 1);
+            mbar_init(&ctl.x_free[i], kMixWarps);
+            mbar_init(&ctl.yz_full[i], 1);
+            mbar_init(&ctl.yz_free[i], 1);
+        }
         for (int i = 0; i < kInfos; ++i) {
             mbar_init(&ctl.info_full[i], 1);
             mbar_init(&ctl.info_free[i], kMixWarps);
@@ -441,38 +556,44 @@ __global__ void __launch_bounds__(kMixThreads, 2)
     if (warp < kMixWarps) {
         const int qw = warp & 3, kh = warp >> 2, row = 32 * qw + lane;
         const uint32_t lanes = tmem + (uint32_t(qw * 32) << 16);
-        bool ok = true;
-        for (int done = 0, step = 0; ok; ++done) {
-            ok = wait_all(&ctl.info_full[done % kInfos], (done / kInfos) & 1, abort_flag);
+        bool ok = wait_warp(&ctl.info_full[0], 0, abort_flag);
+        for (int done = 0, step = 0, tile = -1; ok; ++done) {
             const MixInfo& I = infos[done % kInfos];
-            if (!ok || I.none) break;
+            if (I.none) break;
             const int n = I.n, nh = I.nh, rev = I.rev, has_m = I.has_m;
             for (int h = 0; h < nh; ++h, ++step) {
-                ok = wait_all(&ctl.s_full, step & 1, abort_flag);
+                ok = wait_warp(&ctl.s_full, step & 1, abort_flag);
                 if (!ok) break;
+                const bool fresh = h > 0 || I.fresh;  // another Y and Z than the step before
+                tile += fresh;
                 tc_fence_after();
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const int jb = 2 * kh + half;
-                    if (rev) decay_scores<true>(lanes + kColS + 32 * jb, I.pw, qw, jb, lane, n);
-                    else decay_scores<false>(lanes + kColS + 32 * jb, I.pw, qw, jb, lane, n);
-                }
+#pragma unroll 1
+                for (int jb = 2 * kh; jb < 2 * kh + 2; ++jb)
+                    decay_scores(lanes + kColS + 32 * jb, I, qw, jb, lane);
                 tmem_st_wait();
                 tc_fence_before();
-                if (I.garbage) {
+                if (I.garbage && fresh) {
                     // rows behind the sequence's end: zero times what lies there has to be zero
-                    ok = wait_all(&ctl.yz_full[step & 1], (step >> 1) & 1, abort_flag);
+                    ok = wait_warp(&ctl.yz_full[tile & 1], (tile >> 1) & 1, abort_flag);
                     if (!ok) break;
-                    zero_rows<kMixWarps * 32>(sm + kMOffYZ + (step & 1) * 2 * kTile + kTile, n);
+                    zero_rows<kMixWarps * 32>(sm + kMOffYZ + (tile & 1) * 2 * kTile + kTile, n);
                     fence_proxy_async();
                 }
+                // P is there; and U and F of the item before have been read
                 warp_arrive(&ctl.p_full);
             }
-            const float bi = rev ? (row < n ? I.pw[kPw0 + n - 1 - row] : 0.f)
-                                 : S.scale * I.pw[kPw0 + row + 1];
-            __nv_bfloat16* out = I.out + row * kD + 32 * kh;
-            ok = ok && wait_all(&ctl.pv_done, (step - 1) & 1, abort_flag);
             if (!ok) break;
+            const float bi = rev ? (row < n ? I.up[kPw0 + n - 1 - row] : 0.f)
+                                 : S.scale * I.up[kPw0 + row + 1];
+            __nv_bfloat16* out = I.out + row * kD + 32 * kh;
+            const CUtensorMap* o = I.o;
+            const int t0 = I.t0 + 32 * qw, plane = I.plane;
+            // the next item's description has been there for long: looked for here, where there is
+            // time
+            ok = wait_warp(&ctl.info_full[(done + 1) % kInfos], ((done + 1) / kInfos) & 1, abort_flag) &&
+                 wait_warp(&ctl.item_done[done & 1], (done >> 1) & 1, abort_flag);
+            if (!ok) break;
+            warp_arrive(&ctl.info_free[done % kInfos]);
             tc_fence_after();
             float u[32];
             tmem_ld32(lanes + kColU + 32 * kh, u);
@@ -488,163 +609,220 @@ __global__ void __launch_bounds__(kMixThreads, 2)
                 for (int x = 0; x < 32; ++x) u[x] *= S.scale;
             }
             tc_fence_before();
-            warp_arrive(&ctl.out_free);
-            if (row < n) {
-                const bool wide = (reinterpret_cast<uintptr_t>(out) & 31) == 0;
+            uint32_t p[16];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    uint32_t p[8];
+            for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(u[2 * x], u[2 * x + 1]);
+            if (o) {
+                // this warp's 32 x 32 tile goes out as one copy, staged (64-byte swizzle) where the
+                // item's X was
+                unsigned char* tile_out = sm + kMOffX + (done & 1) * kTile + warp * 2048;
+                const uint32_t at = smem_u32(tile_out) + lane * 64, sw = (lane >> 1) & 3;
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        p[x] = pack_bf16x2(u[16 * half + 2 * x], u[16 * half + 2 * x + 1]);
-                    store16(out + 16 * half, p, wide);
+                for (int x = 0; x < 4; ++x)
+                    sts128(at + ((x ^ sw) << 4), p[4 * x], p[4 * x + 1], p[4 * x + 2], p[4 * x + 3]);
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    if (32 * qw < n) {
+                        tma_store_3d(o, tile_out, 32 * kh, t0, plane);
+                        bulk_commit();
+                        bulk_wait_read0();
+                    }
+                    mbar_arrive(&ctl.x_free[done & 1]);
                 }
+            } else {
+                if (row < n)
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        reinterpret_cast<uint4*>(out)[x] =
+                            make_uint4(p[4 * x], p[4 * x + 1], p[4 * x + 2], p[4 * x + 3]);
+                warp_arrive(&ctl.x_free[done & 1]);
             }
-            warp_arrive(&ctl.info_free[done % kInfos]);
         }
+        if (lane == 0) bulk_wait0();
     } else if (warp == kAheadWarp) {
-        int nx = 0, nm = 0, nyz = 0, done = 0;
-        bool ok = true, waited = false;
-        for (int idx = blockIdx.x;; idx += gridDim.x, ++done) {
-            MixItem it;
-            it.n = 0;
-            for (; idx < items; idx += gridDim.x)
-                if ((it = mix_item(jobs, S, idx)).n > 0) break;
+        int nx = 0, nm = 0, nyz = 0;
+        bool ok = true, waited = false, fresh = true;
+        MixWalk at;
+        at.start(jobs, S, lane);
+        for (int done = 0;; ++done) {
             if (done >= kInfos)
-                ok = wait_all_sleep(&ctl.info_free[done % kInfos], (done / kInfos - 1) & 1, abort_flag);
+                ok = wait_warp(&ctl.info_free[done % kInfos], (done / kInfos - 1) & 1, abort_flag);
             if (!ok) break;
             MixInfo& I = infos[done % kInfos];
-            const bool none = idx >= items;
-            const MixJob& J = jobs.job[it.n > 0 ? it.w : 0];
-            if (!none) {
-                const float g = decay_log(S.log_decay, it.kv);
-                I.pw[1 + lane] = 0.f;
-                #pragma unroll
-                for (int i = 0; i < kC; i += 32) I.pw[kPw0 + i + lane] = decay_pow(g, i + lane);
-                if (lane == 0) I.pw[kPw0 + kC] = decay_pow(g, kC);
+            if (!at.more()) {
                 if (lane == 0) {
-                    const int left = S.T - it.c * kC, plane = it.b * J.j.hx + it.hx;
-                    I.out = static_cast<__nv_bfloat16*>(J.j.out) +
-                            (size_t(plane) * S.T + it.c * kC) * kD;
-                    I.n = it.n;
-                    I.nh = it.nh;
-                    I.rev = J.j.rev;
-                    I.has_m = it.has_m;
-                    I.mem_t = J.j.mem_t;
-                    I.garbage = it.n < kC && it.n < left;
+                    I.none = 1;
+                    if (nx >= 2)
+                        ok = wait(&ctl.x_free[nx & 1], ((nx >> 1) - 1) & 1, abort_flag);
+                    if (ok) mbar_arrive(&ctl.x_full[nx & 1]);
                 }
+                warp_arrive(&ctl.info_full[done % kInfos]);
+                break;
             }
-            if (lane == 0) I.none = none;
-            warp_arrive(&ctl.info_full[done % kInfos]);
-            if (none) break;
+            const MixJob& J = jobs.job[at.w];
+            const int grp = MixWalk::heads(J.j, S.Hkv), nh = MixWalk::steps(J.j);
+            const int b = at.b, c = at.c, kv = at.kv, hx = kv * grp + at.gi, left = S.T - c * kC;
+            const int plane = b * J.j.hx + hx;
+            const int y0 = b * J.j.hy + (nh > 1 ? hx * nh : J.j.hy == J.j.hx ? hx : kv);
+            const int n = min(kC, at.len - c * kC);
+            const bool has_m = c != (J.j.rev ? (at.len - 1) / kC : 0) || J.has_first;
+            const bool shares = nh == 1 && J.j.hy < J.j.hx;  // the group's heads share Y, Z and M
+            const float g = decay_log(S.log_decay, kv);
+            const bool first = fresh;
+            const int gi = at.gi;
+            at.advance(jobs, S, lane);
+            const bool last = !shares || gi + 1 == grp || !at.more();
+#pragma unroll 1
+            for (int i = 0; i < kC; i += 32) {
+                const float l = decay_pow(g, i + lane);
+                I.up[kPw0 + i + lane] = l;
+                I.down[kPw0 + 127 - i - lane] = l;
+            }
             if (lane == 0) {
-                // Y and Z of a step go where those of two steps before were, once P Z has read them
-                // (a barrier of each stage: this warp may lag behind pv_done by two phases, which
-                // a parity cannot tell from none)
+                I.up[kPw0 + kC] = decay_pow(g, kC);
+                I.out = static_cast<__nv_bfloat16*>(J.j.out) + (size_t(plane) * S.T + c * kC) * kD;
+                I.o = n == min(kC, left) ? &J.o : nullptr;
+                I.t0 = c * kC;
+                I.plane = plane;
+                I.n = n;
+                I.nh = nh;
+                I.rev = J.j.rev;
+                I.has_m = has_m;
+                I.mem_t = J.j.mem_t;
+                I.garbage = n < kC && n < left;
+                I.none = 0;
+                I.fresh = first;
+                I.last = last;
+            }
+            warp_arrive(&ctl.info_full[done % kInfos]);
+            fresh = last;
+            if (lane == 0) {
+                if (nx >= 2) ok = wait(&ctl.x_free[nx & 1], ((nx >> 1) - 1) & 1, abort_flag);
+                if (ok) {
+                    uint64_t* bar = &ctl.x_full[nx & 1];
+                    mbar_expect_tx(bar, kTile);
+                    tma_load_3d(sm + kMOffX + (nx & 1) * kTile, &J.x, bar, 0, c * kC, plane);
+                    ++nx;
+                }
                 auto load_yz = [&](int h) {
                     if (nyz >= 2)
-                        ok = mbar_wait_sleep(&ctl.yz_free[nyz & 1], ((nyz >> 1) - 1) & 1, abort_flag);
+                        ok = wait(&ctl.yz_free[nyz & 1], ((nyz >> 1) - 1) & 1, abort_flag);
                     if (!ok) return;
                     unsigned char* dst = sm + kMOffYZ + (nyz & 1) * 2 * kTile;
                     uint64_t* bar = &ctl.yz_full[nyz & 1];
-                    const int plane = it.b * J.j.hy + it.y0 + h;
                     mbar_expect_tx(bar, 2 * kTile);
-                    tma_load_3d(dst, &J.y, bar, 0, it.c * kC, plane);
-                    tma_load_3d(dst + kTile, &J.z, bar, 0, it.c * kC, plane);
+                    tma_load_3d(dst, &J.y, bar, 0, c * kC, y0 + h);
+                    tma_load_3d(dst + kTile, &J.z, bar, 0, c * kC, y0 + h);
                     ++nyz;
                 };
-                if (done > 0) ok = mbar_wait_sleep(&ctl.x_free, (done - 1) & 1, abort_flag);
-                if (ok) {
-                    mbar_expect_tx(&ctl.x_full, kTile);
-                    tma_load_3d(sm + kMOffX, &J.x, &ctl.x_full, 0, it.c * kC, it.b * J.j.hx + it.hx);
-                    ++nx;
-                    load_yz(0);
-                }
+                if (ok && first) load_yz(0);
                 // (the inputs were there before the kernels whose results this one waits for)
                 if (!waited) grid_dep_wait();
                 waited = true;
-                if (ok && it.has_m) {
-                    mbar_expect_tx(&ctl.m_full, kMTile);
-                    tma_load_2d(sm + kMOffM, &J.m, &ctl.m_full, 0,
-                                ((it.b * S.Hkv + it.kv) * S.chunks + it.c) * 64);
-                    ++nm;
+                if (ok && first && has_m) {
+                    if (nm >= 1) ok = wait(&ctl.m_free, (nm - 1) & 1, abort_flag);
+                    if (ok) {
+                        mbar_expect_tx(&ctl.m_full, kMTile);
+                        tma_load_2d(sm + kMOffM, &J.m, &ctl.m_full, 0,
+                                    ((b * S.Hkv + kv) * S.chunks + c) * 64);
+                        ++nm;
+                    }
                 }
-                for (int h = 1; ok && h < it.nh; ++h) load_yz(h);
+                for (int h = 1; ok && h < nh; ++h) load_yz(h);
             }
             ok = __shfl_sync(~0u, ok ? 1 : 0, 0) != 0;
             if (!ok) break;
         }
         if (lane == 0) {
             if (!waited) grid_dep_wait();
-            // no copy is in flight when the CTA ends
-            if (nx) bounded_spin_done(&ctl.x_full, (nx - 1) & 1);
-            if (nm) bounded_spin_done(&ctl.m_full, (nm - 1) & 1);
-            if (nyz) bounded_spin_done(&ctl.yz_full[(nyz - 1) & 1], ((nyz - 1) >> 1) & 1);
-            if (nyz > 1) bounded_spin_done(&ctl.yz_full[nyz & 1], ((nyz - 2) >> 1) & 1);
+            // no copy is in flight when the CTA ends: the MMA warp has waited for each, unless
+            // this warp gave up
+            for (int k = 1; !ok && k <= 2; ++k) {
+                if (nx >= k) bounded_spin_done(&ctl.x_full[(nx - k) & 1], ((nx - k) >> 1) & 1);
+                if (nyz >= k) bounded_spin_done(&ctl.yz_full[(nyz - k) & 1], ((nyz - k) >> 1) & 1);
+            }
+            if (!ok && nm) bounded_spin_done(&ctl.m_full, (nm - 1) & 1);
         }
     } else if (lane == 0) {
         constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
         constexpr uint32_t id_mn = idesc_bf16(128, 64, false, true), id_k = idesc_bf16(128, 64, false, false);
-        const uint32_t x = smem_u32(sm + kMOffX), m = smem_u32(sm + kMOffM);
-        const uint32_t yz = smem_u32(sm + kMOffYZ);
-        int nm = 0, npv = 0, nfree = 0, step = 0;
+        const uint32_t m = smem_u32(sm + kMOffM);
+        int nm = 0, step = 0, tile = -1;
         bool ok = true;
+        // Every wait and every commit of this thread costs a few hundred cycles of the chain from
+        // one item to the next, so it has few: three waits and two commits for an item of one step
+        // that shares its tiles with the item before.
+        // What it can look at early (the next item's description and whether its X is there), it
+        // looks at while the compute warps work on the scores.
+        struct Next {
+            int none, nh, has_m, mem_t, first, last;
+        };
+        auto read = [&](int k) {
+            const MixInfo& I = infos[k % kInfos];
+            return Next{I.none, I.nh, I.has_m, I.mem_t, I.fresh, I.last};
+        };
+        ok = wait(&ctl.x_full[0], 0, abort_flag);
+        Next it = read(0);
+        bool ready = true;  // X of the present item has been seen
         for (int done = 0; ok; ++done) {
-            ok = mbar_wait(&ctl.info_full[done % kInfos], (done / kInfos) & 1, abort_flag);
-            const MixInfo& I = infos[done % kInfos];
-            if (!ok || I.none) break;
-            const int nh = I.nh, has_m = I.has_m, mem_t = I.mem_t;
-            ok = mbar_wait(&ctl.x_full, done & 1, abort_flag);
-            for (int h = 0; ok && h < nh; ++h, ++step) {
-                ok = mbar_wait(&ctl.yz_full[step & 1], (step >> 1) & 1, abort_flag) &&
-                     // the scores go over P of the step before
-                     (step == 0 || mbar_wait(&ctl.pv_done, (step - 1) & 1, abort_flag));
+            if (!ready) {
+                ok = wait(&ctl.x_full[done & 1], (done >> 1) & 1, abort_flag);
+                it = read(done);
+            }
+            if (!ok || it.none) break;
+            const Next now = it;
+            ready = false;
+            const uint32_t x = smem_u32(sm + kMOffX + (done & 1) * kTile);
+            for (int h = 0; ok && h < now.nh; ++h, ++step) {
+                if (h > 0 || now.first) {
+                    ++tile;
+                    ok = wait(&ctl.yz_full[tile & 1], (tile >> 1) & 1, abort_flag);
+                }
+                // the scores go over P of the step before
+                if (ok && h > 0) ok = wait(&ctl.yz_free[(tile - 1) & 1], ((tile - 1) >> 1) & 1, abort_flag);
+                else if (ok && done > 0)
+                    ok = wait(&ctl.item_done[(done - 1) & 1], ((done - 1) >> 1) & 1, abort_flag);
                 if (!ok) break;
-                const uint32_t y = yz + (step & 1) * 2 * kTile, z = y + kTile;
-                tc_fence_after();
-#pragma unroll
+                const uint32_t y = smem_u32(sm + kMOffYZ) + (tile & 1) * 2 * kTile, z = y + kTile;
+#pragma unroll 1
                 for (int ks = 0; ks < 4; ++ks)
                     mma_bf16(tmem + kColS, sdesc_sw128(x + ks * 32, 16, 1024),
                              sdesc_sw128(y + ks * 32, 16, 1024), id_s, ks > 0 ? 1u : 0u);
                 mma_commit(&ctl.s_full);
-                if (h == 0) {
-                    // U and F of the item before have been read
-                    if (done > 0) ok = mbar_wait(&ctl.out_free, (done - 1) & 1, abort_flag);
-                    if (ok && has_m) {
-                        ok = mbar_wait(&ctl.m_full, nm & 1, abort_flag);
-                        ++nm;
-                        if (ok) {
-                            tc_fence_after();
-#pragma unroll
-                            for (int ks = 0; ks < 4; ++ks)
-                                mma_bf16(tmem + kColF, sdesc_sw128(x + ks * 32, 16, 1024),
-                                         mem_t ? sdesc_sw128(m + ks * 32, 16, 1024)
-                                               : sdesc_sw128(m + ks * 2048, kTile, 1024),
-                                         mem_t ? id_k : id_mn, ks > 0 ? 1u : 0u);
-                        }
-                    }
+                if (h == 0 && now.has_m && now.first) {
+                    ok = wait(&ctl.m_full, nm & 1, abort_flag);
+                    ++nm;
                     if (!ok) break;
                 }
-                if (h == nh - 1) {
-                    mma_commit(&ctl.x_free);  // no later MMA of the item reads X or M
-                    ++nfree;
+                if (h == now.nh - 1 &&
+                    mbar_try_wait(&ctl.x_full[(done + 1) & 1], ((done + 1) >> 1) & 1)) {
+                    ready = true;
+                    it = read(done + 1);
                 }
-                ok = mbar_wait(&ctl.p_full, step & 1, abort_flag);
+                ok = wait(&ctl.p_full, step & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                 for (int ks = 0; ks < 8; ++ks)
                     mma_bf16_ts(tmem + kColU, tmem + kColS + 32 * (ks >> 1) + 8 * (ks & 1),
                                 sdesc_sw128(z + ks * 2048, kTile, 1024), id_mn,
                                 (h > 0 || ks > 0) ? 1u : 0u);
-                mma_commit(&ctl.pv_done);
-                mma_commit(&ctl.yz_free[step & 1]);
-                ++npv;
+                if (h == 0 && now.has_m) {
+                    const uint32_t id = now.mem_t ? id_k : id_mn, by = now.mem_t ? 32 : 2048;
+#pragma unroll 1
+                    for (int ks = 0; ks < 4; ++ks)
+                        mma_bf16(tmem + kColF, sdesc_sw128(x + ks * 32, 16, 1024),
+                                 sdesc_sw128(m + ks * by, kTile, 1024), id, ks > 0 ? 1u : 0u);
+                    if (now.last) mma_commit(&ctl.m_free);
+                }
+                if (h == now.nh - 1) mma_commit(&ctl.item_done[done & 1]);
+                if (h < now.nh - 1 || now.last) mma_commit(&ctl.yz_free[tile & 1]);
             }
         }
-        // every MMA has completed before tensor memory is freed
-        if (nfree) bounded_spin_done(&ctl.x_free, (nfree - 1) & 1);
-        if (npv) bounded_spin_done(&ctl.yz_free[(npv - 1) & 1], ((npv - 1) >> 1) & 1);
+        // every MMA has completed before tensor memory is freed (a commit covers all before it)
+        mma_commit(&ctl.drained);
+        bounded_spin_done(&ctl.drained, 0);
     }
     __syncwarp();
     tc_fence_before();

@@ -30,7 +30,9 @@ def clean():
 
 SHAPES = [(1, 1, 1, 1), (2, 2, 2, 1), (1, 63, 7, 1), (2, 64, 6, 3), (1, 65, 8, 1), (3, 127, 2, 2),
           (1, 128, 14, 2), (2, 129, 4, 4), (1, 255, 3, 1), (2, 300, 14, 2), (1, 1000, 5, 5),
-          (1, 2049, 4, 2), (1, 1000, 56, 8)]  # the last: a group of 7 summed in uneven parts
+          (1, 2049, 4, 2),
+          (1, 1000, 56, 8),   # a group of 7 summed in uneven parts
+          (2, 1100, 28, 4)]   # several query heads in a row per block, which share their tiles
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
@@ -87,6 +89,31 @@ def test_padded_batch(cuda, dtype):
             assert bool((x[b, :, n:] == 3.0).all())
     fresh, state = oal.decay_prefill(q, k, v, g, SCALE, lens=ln)
     assert bool((fresh[1] == 0).all()) and bool((state[1] == 0).all())
+    clean()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_padded_batch_of_many(cuda, dtype):
+    """70 sequences of all lengths, runs of empty ones among them."""
+    gen = torch.Generator().manual_seed(3)
+    lens = torch.randint(0, 401, (70,), generator=gen)
+    lens[5:44] = 0
+    lens[[0, 69]] = 0
+    lens[50] = 400
+    q, k, v, g, do, S, R = make(cuda, 70, 400, 14, 2, dtype, state=True)
+    ln = lens.to(torch.int32).to(cuda)
+    held = S.clone()
+    out = oal.decay_prefill_continue(q, k, v, g, SCALE, held, lens=ln)
+    w = ref.forward(q, k, v, g, SCALE, lens=lens, state=S)
+    ref.check("out", out, w[0], w[2], dtype, 400)
+    ref.check("state", held, w[1], w[3], F32, 400)
+    got = oal.decay_backward(q, k, v, g, SCALE, do, lens=ln, state=S, dlast=R)
+    w = ref.backward(q, k, v, g, SCALE, do, lens=lens, state=S, dlast=R)
+    for n, (x, size) in w.items():
+        ref.check(n, got[n], x, size, F32 if n == "dstate" else dtype, 400)
+    none = torch.zeros_like(ln)
+    out, state = oal.decay_prefill(q, k, v, g, SCALE, lens=none)
+    assert bool((out == 0).all()) and bool((state == 0).all())
     clean()
 
 
