@@ -42,14 +42,21 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
     const int c = blockIdx.x, bkv = blockIdx.y, b = bkv / S.Hkv, kv = bkv % S.Hkv;
     tc::grid_dep_launch();
     const int n = min(kC, decay_len(S, b) - c * kC);
-    if (n <= 0) return;  // the scan does not read it
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    if (n <= 0) {  // the scan does not read it
+        if (S.chunks == 1)
+            for (int i = 0; i < 4; ++i)
+                scan_one<float>(J, bkv, (4 * ty + i) * kDV + 4 * tx, 1.f,
+                                make_float4(0.f, 0.f, 0.f, 0.f));
+        return;
+    }
     __shared__ __align__(16) float Y[kC][kLd], Z[kC][kLd];
     __shared__ float w[kC];
     const float g = decay_log(S.log_decay, kv);
     if (threadIdx.x < kC)
         w[threadIdx.x] = J.rev ? S.scale * decay_pow(g, threadIdx.x + 1)
                                : decay_pow(g, max(0, n - 1 - int(threadIdx.x)));
-    const int grp = J.hy / S.Hkv, ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int grp = J.hy / S.Hkv;
     float acc[4][4] = {};
     for (int h = 0; h < grp; ++h) {
         const size_t plane = (size_t(b) * J.hy + kv * grp + h) * S.T * kD;
@@ -70,9 +77,12 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
     }
     float* out = J.delta + (size_t(bkv) * S.chunks + c) * kDecayState;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<float4*>(out + (4 * ty + i) * kDV + 4 * tx) =
-            make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+    for (int i = 0; i < 4; ++i) {
+        const int e = (4 * ty + i) * kDV + 4 * tx;
+        const float4 sum = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        if (S.chunks > 1) *reinterpret_cast<float4*>(out + e) = sum;
+        else scan_one<float>(J, bkv, e, decay_pow(g, n), sum);
+    }
 }
 
 // ------------------------------------------------------------------------------------------
@@ -359,7 +369,7 @@ constexpr int kSms = 148;
 int parts_of(const oal_shape* s, int grp)
 {
     const long long items = (long long)s->B * s->Hkv * chunks_of(s);
-    if (!on_tensor_cores(s) || items == 0) return 1;
+    if (!on_tensor_cores(s) || chunks_of(s) <= 1) return 1;
     const int parts = int(std::min<long long>(grp, (2 * kSms + items - 1) / items));
     const int per = (grp + parts - 1) / parts;
     return (grp + per - 1) / per;  // none of them empty
@@ -439,7 +449,7 @@ bool make_state_map(CUtensorMap* m, const void* base, size_t planes)
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The sums of `n` directions (1 or 2) and their scans.
+// The sums of `n` directions (1 or 2) and their scans.  (A sequence of one chunk needs no scan.)
 int launch_sums(const DecayShape& S, const DecaySum* a, int n, const oal_shape* s, cudaStream_t st)
 {
     const DecaySum& b2 = a[n - 1];
@@ -449,12 +459,12 @@ int launch_sums(const DecayShape& S, const DecaySum* a, int n, const oal_shape* 
         if (on_tensor_cores(s)) {
             dtc::SumMaps maps;
             int items = 0;
-            for (int i = 0; i < 2; ++i) {
-                const DecaySum& j = i < n ? a[i] : a[0];
+            for (int i = 0; i < n; ++i) {
+                const DecaySum& j = a[i];
                 if (!make_map_uncached(&maps.y[i], j.y, s->T, s->B * j.hy) ||
                     !make_map_uncached(&maps.z[i], j.z, s->T, s->B * j.hy))
                     return OAL_ERR_CUDA;
-                if (i < n) items += j.parts * planes * S.chunks;
+                items += j.parts * planes * S.chunks;
             }
             dtc::delta_kernel<<<items, dtc::kThreads, dtc::kDeltaSmem, st>>>(maps, S, a[0], b2);
         } else {
@@ -462,6 +472,7 @@ int launch_sums(const DecayShape& S, const DecaySum* a, int n, const oal_shape* 
         }
         OAL_LAUNCH_CHECK();
     }
+    if (S.chunks == 1) return OAL_OK;  // there is nothing to scan
     LaunchScope ls("decay_scan", st);
     OAL_CUDA_TRY(launch_ex(on_tensor_cores(s) ? scan_kernel<__nv_bfloat16> : scan_kernel<float>,
                            dim3(kDecayState / kScanCols, planes, n), dim3(kThreads), 0, st,

@@ -19,6 +19,7 @@
 #pragma once
 
 #include "oal_common.cuh"
+#include "oal_tc_util.cuh"
 
 namespace oal {
 
@@ -77,6 +78,27 @@ __device__ __forceinline__ float decay_pow(float g, int m)
 {
     const float fm = float(m), p = fm * g;
     return expf(p) * (1.f + fmaf(fm, g, -p));
+}
+
+__device__ __forceinline__ void store_state(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
+__device__ __forceinline__ void store_state(__nv_bfloat16* p, float4 v)
+{
+    *reinterpret_cast<uint2*>(p) =
+        make_uint2(tc::pack_bf16x2(v.x, v.y), tc::pack_bf16x2(v.z, v.w));
+}
+
+// The scan of a sequence of one chunk, done by the kernel that has the chunk's sum: entries e .. e + 3.
+template <typename Tm>
+__device__ __forceinline__ void scan_one(const DecaySum& J, int bkv, int e, float l, float4 sum)
+{
+    const size_t at = size_t(bkv) * kDecayState + e;
+    float4 cur = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (J.first) cur = *reinterpret_cast<const float4*>(J.first + at);
+    store_state(static_cast<Tm*>(J.mem) + at, cur);
+    if (J.last)
+        *reinterpret_cast<float4*>(J.last + at) =
+            make_float4(fmaf(l, cur.x, sum.x), fmaf(l, cur.y, sum.y), fmaf(l, cur.z, sum.z),
+                        fmaf(l, cur.w, sum.w));
 }
 
 // Tokens of sequence b.

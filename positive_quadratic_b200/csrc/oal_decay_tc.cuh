@@ -6,7 +6,6 @@
 #pragma once
 
 #include "oal_decay.cuh"
-#include "oal_tc_util.cuh"
 
 namespace oal {
 namespace decay {
@@ -221,7 +220,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int e = i * 256 + threadIdx.x;
-                    out[e] = *reinterpret_cast<const float4*>(&stage[e >> 4][4 * (e & 15)]);
+                    const float4 sum = *reinterpret_cast<const float4*>(&stage[e >> 4][4 * (e & 15)]);
+                    if (S.chunks > 1) out[e] = sum;
+                    else scan_one<__nv_bfloat16>(J, bkv, 4 * e, decay_pow(decay_log(S.log_decay, kv), n), sum);
                 }
                 tc_fence_before();
             }
@@ -273,6 +274,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (nmma) bounded_spin_done(&ctl.done, (nmma - 1) & 1);
         }
     }
+    if (n <= 0 && S.chunks == 1 && warp < 8)
+        for (int e = threadIdx.x; e < kDecayState / 4; e += 256)
+            scan_one<__nv_bfloat16>(J, bkv, 4 * e, 1.f, make_float4(0.f, 0.f, 0.f, 0.f));
     __syncwarp();
     tc_fence_before();
     __syncthreads();

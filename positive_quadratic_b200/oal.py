@@ -7,6 +7,7 @@ when the library is missing.  There is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import re
 import threading
@@ -604,22 +605,8 @@ def backward_workspace(q, k, v) -> torch.Tensor:
     return empty_workspace(n.value, q.device)
 
 
-class _Here:
-    """A call on the current device and its current stream: nothing to switch."""
-    __slots__ = ("stream",)
-
-    def __init__(self, stream):
-        self.stream = stream
-
-    def __enter__(self):
-        return self.stream
-
-    def __exit__(self, *exc):
-        pass
-
-
 class _There:
-    """A call on another device or stream, which are current inside."""
+    """Another device or stream than the current ones, which become current inside."""
 
     def __init__(self, device, stream):
         self.ctx = [torch.cuda.device(device)]
@@ -629,57 +616,67 @@ class _There:
     def __enter__(self):
         for c in self.ctx:
             c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         for c in reversed(self.ctx):
             c.__exit__(*exc)
 
 
-def _on(device, stream):
-    """The device and stream of a call, as a context that gives the stream's handle.  Tensors made
-    inside belong to that stream, so that their memory is not handed out again before the call's
+def _call_on_stream(f):
+    """Lets the calls below run on the current stream of the device of their first argument: a
+    call for another device or stream makes those current around itself, so that the tensors it
+    makes belong to that stream, and their memory is not handed out again before the call's
     kernels are done with it."""
-    index = device.index
-    if stream is None and index == torch._C._cuda_getDevice():
-        return _Here(torch._C._cuda_getCurrentRawStream(index))
-    return _There(device, stream)
+    first = f.__code__.co_varnames[0]
+
+    @functools.wraps(f)
+    def call(*args, stream=None, **kwargs):
+        x = args[0] if args else kwargs[first]
+        index = x.get_device()
+        if index < 0:
+            raise ValueError("tensors must be contiguous CUDA tensors")
+        if stream is None and index == torch._C._cuda_getDevice():
+            return f(*args, stream=torch._C._cuda_getCurrentRawStream(index), **kwargs)
+        with _There(x.device, stream):
+            return f(*args, stream=torch._C._cuda_getCurrentRawStream(index), **kwargs)
+    return call
 
 
-def _need(name, t, shape, dtype, device, optional=False):
-    """Refuses a tensor that is not a contiguous CUDA tensor of this shape, type and device."""
-    if t is None:
-        if optional:
-            return None
-        raise ValueError(f"{name} is missing")
+def _need(name, t, shape, dtype, index):
+    """Pointer of a contiguous tensor of this shape and type on CUDA device `index`; refuses any
+    other."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if not t.is_cuda or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be a contiguous CUDA tensor on cuda:{index}")
 
 
-def _need_ws(ws, device):
-    if ws.device != device or not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous CUDA tensor on {device}")
+def _need_ws(ws, index):
+    if ws.get_device() != index or not ws.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous CUDA tensor on cuda:{index}")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
+_CODE = {torch.bfloat16: OAL_BF16, torch.float32: OAL_F32}
+
+
 def _decay_args(q, k, v, log_decay, lens):
-    """(shape, the pointers of q, k, v, log_decay, lens) of a decayed linear attention call."""
+    """(shape, sizes, the pointers of q, k, v, log_decay, lens) of a decayed linear attention
+    call; sizes: of q, of k and v, of the state."""
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k, v must be [B, H, T, 64]")
-    B, Hq, T, d = q.shape
+    dt, index, qs = q.dtype, q.get_device(), q.shape
+    B, Hq, T, d = qs
     Hkv = k.shape[1]
-    shape = Shape(B, T, Hq, Hkv, d, v.shape[-1], 128, _dtype_code(q))
-    dev = q.device
     kv = (B, Hkv, T, d)
-    return shape, (_need("q", q, q.shape, q.dtype, dev), _need("k", k, kv, q.dtype, dev),
-                   _need("v", v, kv, q.dtype, dev),
-                   _need("log_decay", log_decay, (Hkv,), torch.float32, dev),
-                   _need("lens", lens, (B,), torch.int32, dev, optional=True))
+    shape = Shape(B, T, Hq, Hkv, d, d, 128, _CODE[dt] if dt in _CODE else _dtype_code(q))
+    return shape, (qs, kv, (B, Hkv, 64, 64), dt, index), (
+        _need("q", q, qs, dt, index), _need("k", k, kv, dt, index), _need("v", v, kv, dt, index),
+        _need("log_decay", log_decay, (Hkv,), torch.float32, index),
+        None if lens is None else _need("lens", lens, (B,), torch.int32, index))
 
 
 def _bytes_of(query, shape) -> int:
@@ -700,26 +697,28 @@ def decay_backward_workspace(q, k, v) -> torch.Tensor:
     return empty_workspace(_bytes_of("oal_decay_backward_workspace_bytes", shape), q.device)
 
 
-def _decay_prefill(name, q, k, v, log_decay, scale, lens, out, state, want_out, workspace, stream,
-                   fresh):
-    shape, (pq, pk, pv, pg, pl) = _decay_args(q, k, v, log_decay, lens)
-    dev = q.device
-    with _on(dev, stream) as s:
-        if out is None and want_out:
+def _decay_prefill(name, q, k, v, log_decay, scale, lens, out, state, want_out, workspace, stream):
+    shape, (qs, _, ss, dt, index), (pq, pk, pv, pg, pl) = _decay_args(q, k, v, log_decay, lens)
+    if not want_out:
+        out = po = None
+    else:
+        if out is None:
             # rows behind a sequence's end are not written
             out = torch.empty_like(q) if lens is None else torch.zeros_like(q)
-        if state is None and fresh:
-            state = torch.empty(shape.B, shape.Hkv, 64, 64, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = empty_workspace(_bytes_of("oal_decay_prefill_workspace_bytes", shape), dev)
-        po = _need("out", out, q.shape, q.dtype, dev, optional=True) if want_out else None
-        ps = _need("state", state, (shape.B, shape.Hkv, 64, 64), torch.float32, dev)
-        pw, nw = _need_ws(workspace, dev)
-        _check(getattr(lib(), name)(pq, pk, pv, pg, scale, pl, po, ps, pw, nw,
-                                    ctypes.byref(shape), s), name)
+        po = _need("out", out, qs, dt, index)
+    if state is None:
+        state = torch.empty(ss, dtype=torch.float32, device=q.device)
+    ps = _need("state", state, ss, torch.float32, index)
+    if workspace is None:
+        workspace = empty_workspace(_bytes_of("oal_decay_prefill_workspace_bytes", shape), q.device)
+    pw, nw = _need_ws(workspace, index)
+    rc = getattr(lib(), name)(pq, pk, pv, pg, scale, pl, po, ps, pw, nw, ctypes.byref(shape), stream)
+    if rc:
+        raise OALError(rc, name)
     return out, state
 
 
+@_call_on_stream
 def decay_prefill(q, k, v, log_decay, scale: float, lens=None, out=None, state=None,
                   want_out: bool = True, workspace=None, stream=None):
     """oal_decay_prefill: linear attention with decay exp(log_decay[kv head]) over prompts
@@ -727,78 +726,81 @@ def decay_prefill(q, k, v, log_decay, scale: float, lens=None, out=None, state=N
     int32: the tokens of each sequence of a padded batch.  Returns (out like q, state
     [B, Hkv, 64, 64] fp32); want_out=False computes the state alone (out is None)."""
     return _decay_prefill("oal_decay_prefill", q, k, v, log_decay, scale, lens, out, state,
-                          want_out, workspace, stream, True)
+                          want_out, workspace, stream)
 
 
+@_call_on_stream
 def decay_prefill_continue(q, k, v, log_decay, scale: float, state, lens=None, out=None,
                            want_out: bool = True, workspace=None, stream=None):
     """oal_decay_prefill_continue: the same from `state`, which is updated; returns out."""
+    if state is None:
+        raise ValueError("decay_prefill_continue needs the state to continue from")
     return _decay_prefill("oal_decay_prefill_continue", q, k, v, log_decay, scale, lens, out,
-                          state, want_out, workspace, stream, False)[0]
+                          state, want_out, workspace, stream)[0]
 
 
+@_call_on_stream
 def decay_step(q, k, v, log_decay, scale: float, state, src=None, parents=None, out=None,
                stream=None):
     """oal_decay_step: one token, q [B, Hq, 1, 64], k and v [B, Hkv, 1, 64]; `state` is updated
     in place, or with src [B', Hkv, 64, 64] and parents (int32, B of them) becomes the state of
     the parents one token on.  Returns out like q."""
-    shape, (pq, pk, pv, pg, _) = _decay_args(q, k, v, log_decay, None)
-    if shape.T != 1:
+    shape, (qs, _, ss, dt, index), (pq, pk, pv, pg, _) = _decay_args(q, k, v, log_decay, None)
+    if qs[2] != 1:
         raise ValueError("decay_step takes one token: q, k, v [B, H, 1, 64]")
-    dev = q.device
-    ps = _need("state", state, (shape.B, shape.Hkv, 64, 64), torch.float32, dev)
+    ps = _need("state", state, ss, torch.float32, index)
     psrc = ppar = None
     n = 0
     if src is not None or parents is not None:
         if src is None or parents is None:
             raise ValueError("src and parents go together")
         n = src.shape[0]
-        psrc = _need("src", src, (n, shape.Hkv, 64, 64), torch.float32, dev)
-        ppar = _parents(parents, shape.B, dev)
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty_like(q)
-        _check(lib().oal_decay_step(pq, pk, pv, pg, scale, psrc, n, ppar, ps,
-                                    _need("out", out, q.shape, q.dtype, dev),
-                                    ctypes.byref(shape), s), "oal_decay_step")
+        psrc = _need("src", src, (n, *ss[1:]), torch.float32, index)
+        ppar = _parents(parents, qs[0], index)
+    if out is None:
+        out = torch.empty_like(q)
+    rc = lib().oal_decay_step(pq, pk, pv, pg, scale, psrc, n, ppar, ps,
+                              _need("out", out, qs, dt, index), ctypes.byref(shape), stream)
+    if rc:
+        raise OALError(rc, "oal_decay_step")
     return out
 
 
+@_call_on_stream
 def decay_backward(q, k, v, log_decay, scale: float, dout, lens=None, state=None, dlast=None,
                    grads=None, dstate=None, workspace=None, stream=None) -> dict:
     """oal_decay_backward: gradients of decay_prefill (state=None) or decay_prefill_continue
     (`state`: the one it started from) for dout like q and dlast = dLoss/d(last state) or None.
     `grads`: (dq, dk, dv) to write to.  Returns dict(dq, dk, dv, dstate)."""
-    shape, (pq, pk, pv, pg, pl) = _decay_args(q, k, v, log_decay, lens)
-    dev = q.device
-    st = (shape.B, shape.Hkv, 64, 64)
-    with _on(dev, stream) as s:
-        if grads is None:
-            # rows behind a sequence's end are not written
-            make = torch.empty_like if lens is None else torch.zeros_like
-            grads = make(q), make(k), make(v)
-        if dstate is None:
-            dstate = torch.empty(st, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = empty_workspace(_bytes_of("oal_decay_backward_workspace_bytes", shape), dev)
-        dq, dk, dv = grads
-        pw, nw = _need_ws(workspace, dev)
-        _check(lib().oal_decay_backward(
-            pq, pk, pv, pg, scale, pl, _need("dout", dout, q.shape, q.dtype, dev),
-            _need("state", state, st, torch.float32, dev, optional=True),
-            _need("dlast", dlast, st, torch.float32, dev, optional=True),
-            _need("dq", dq, q.shape, q.dtype, dev), _need("dk", dk, k.shape, q.dtype, dev),
-            _need("dv", dv, v.shape, q.dtype, dev),
-            _need("dstate", dstate, st, torch.float32, dev), pw, nw, ctypes.byref(shape), s),
-            "oal_decay_backward")
+    shape, (qs, kv, ss, dt, index), (pq, pk, pv, pg, pl) = _decay_args(q, k, v, log_decay, lens)
+    f32 = torch.float32
+    if grads is None:
+        # rows behind a sequence's end are not written
+        make = torch.empty_like if lens is None else torch.zeros_like
+        grads = make(q), make(k), make(v)
+    if dstate is None:
+        dstate = torch.empty(ss, dtype=f32, device=q.device)
+    if workspace is None:
+        workspace = empty_workspace(_bytes_of("oal_decay_backward_workspace_bytes", shape), q.device)
+    dq, dk, dv = grads
+    pw, nw = _need_ws(workspace, index)
+    rc = lib().oal_decay_backward(
+        pq, pk, pv, pg, scale, pl, _need("dout", dout, qs, dt, index),
+        None if state is None else _need("state", state, ss, f32, index),
+        None if dlast is None else _need("dlast", dlast, ss, f32, index),
+        _need("dq", dq, qs, dt, index), _need("dk", dk, kv, dt, index),
+        _need("dv", dv, kv, dt, index), _need("dstate", dstate, ss, f32, index), pw, nw,
+        ctypes.byref(shape), stream)
+    if rc:
+        raise OALError(rc, "oal_decay_backward")
     return dict(dq=dq, dk=dk, dv=dv, dstate=dstate)
 
 
-def _parents(parents, B, dev):
+def _parents(parents, B, index):
     """Pointer of `parents`, int32, B of them in any shape ([B] or [searches, beams])."""
     if parents.numel() != B:
         raise ValueError(f"parents must hold {B} indices, got {parents.numel()}")
-    return _need("parents", parents, parents.shape, torch.int32, dev)
+    return _need("parents", parents, parents.shape, torch.int32, index)
 
 
 def beam_select_workspace(B, beams, V, n, device, dtype=torch.float32) -> torch.Tensor:
@@ -813,6 +815,7 @@ def _select_bytes(B, beams, V, n, code) -> int:
     return nb.value
 
 
+@_call_on_stream
 def beam_select(logits, running, n: int, ended=None, pad_token: int = 0, scores=None,
                 parents=None, tokens=None, workspace=None, stream=None):
     """oal_beam_select: of logits [B, beams, V] (bf16 or fp32; rows may lie further apart than V)
@@ -822,101 +825,105 @@ def beam_select(logits, running, n: int, ended=None, pad_token: int = 0, scores=
     if logits.dim() != 3:
         raise ValueError("logits must be [B, beams, V]")
     B, beams, V = logits.shape
-    dev = logits.device
-    ld = logits.stride(1) if beams > 1 else (logits.stride(0) if B > 1 else V)
-    if not logits.is_cuda or (V > 1 and logits.stride(2) != 1) or ld < V or (
-            B > 1 and logits.stride(0) != beams * ld):
-        raise ValueError("logits must be a CUDA tensor whose rows are contiguous and equally "
-                         "spaced")
+    index = logits.get_device()
+    if logits.is_contiguous():
+        ld = V
+    else:
+        ld = logits.stride(1) if beams > 1 else (logits.stride(0) if B > 1 else V)
+        if (V > 1 and logits.stride(2) != 1) or ld < V or (B > 1 and logits.stride(0) != beams * ld):
+            raise ValueError("logits' rows must be contiguous and equally spaced")
     if ended is not None and ended.dtype is torch.bool:
         ended = ended.view(torch.uint8)
-    code = _dtype_code(logits)
-    pr = _need("running", running, (B, beams), torch.float32, dev)
-    pe = _need("ended", ended, (B, beams), torch.uint8, dev, optional=True)
-    with _on(dev, stream) as s:
-        if scores is None:
-            scores = torch.empty(B, n, dtype=torch.float32, device=dev)
-        if parents is None:
-            parents = torch.empty(B, n, dtype=torch.int32, device=dev)
-        if tokens is None:
-            tokens = torch.empty(B, n, dtype=torch.int32, device=dev)
-        if workspace is None:
-            workspace = empty_workspace(_select_bytes(B, beams, V, n, code), dev)
-        pw, nw = _need_ws(workspace, dev)
-        _check(lib().oal_beam_select(
-            logits.data_ptr(), ld, code, pr, pe, pad_token, B, beams, V, n,
-            _need("scores", scores, (B, n), torch.float32, dev),
-            _need("parents", parents, (B, n), torch.int32, dev),
-            _need("tokens", tokens, (B, n), torch.int32, dev), pw, nw, s), "oal_beam_select")
+    dt = logits.dtype
+    code = _CODE[dt] if dt in _CODE else _dtype_code(logits)
+    rows, best, i32 = (B, beams), (B, n), torch.int32
+    if scores is None:
+        scores = torch.empty(best, dtype=torch.float32, device=logits.device)
+    if parents is None and tokens is None:
+        parents, tokens = torch.empty((2, B, n), dtype=i32, device=logits.device).unbind(0)
+    elif parents is None:
+        parents = torch.empty(best, dtype=i32, device=logits.device)
+    elif tokens is None:
+        tokens = torch.empty(best, dtype=i32, device=logits.device)
+    if workspace is None:
+        workspace = empty_workspace(_select_bytes(B, beams, V, n, code), logits.device)
+    pw, nw = _need_ws(workspace, index)
+    rc = lib().oal_beam_select(
+        logits.data_ptr(), ld, code, _need("running", running, rows, torch.float32, index),
+        None if ended is None else _need("ended", ended, rows, torch.uint8, index), pad_token, B,
+        beams, V, n, _need("scores", scores, best, torch.float32, index),
+        _need("parents", parents, best, i32, index), _need("tokens", tokens, best, i32, index), pw,
+        nw, stream)
+    if rc:
+        raise OALError(rc, "oal_beam_select")
     return scores, parents, tokens
 
 
-def _state_of(name, t, B, Hq, Hkv, dev):
-    """Pointer of a state buffer (uint8) of B sequences; B None: as many as it has room for."""
+def _state_of(name, t, B, Hq, Hkv, index):
+    """(pointer, sequences) of a state buffer (uint8) with room for B sequences at least."""
     if t.dtype is not torch.uint8 or t.dim() != 1:
         raise TypeError(f"{name} must be a state buffer (uint8, one dimension)")
-    if t.device != dev or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on {dev}")
+    if t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on cuda:{index}")
     # the layout of oal_state_bytes: header and coefficient tables, then the sequences
-    empty = 256 + (Hq * FEATURES_PAD * 4 + 255) // 256 * 256
-    one = Hkv * FEATURES_PAD * (VALUE_DIM + 1) * 4
-    held = (t.numel() - empty) // one
-    if t.numel() < empty or (B is not None and held < B):
+    held = (t.numel() - 256 - (Hq * FEATURES_PAD * 4 + 255) // 256 * 256) // (
+        Hkv * FEATURES_PAD * (VALUE_DIM + 1) * 4)
+    if held < B:
         raise ValueError(f"{name} holds {t.numel()} bytes, too few for its sequences")
     return t.data_ptr(), held
 
 
+@_call_on_stream
 def state_reorder(src, parents, dst, Hq: int, Hkv: int, stream=None):
     """oal_state_reorder: sequence i of the state buffer dst becomes sequence parents[i] (int32)
     of the state buffer src; dst has as many sequences as there are parents.  Returns dst."""
-    dev = src.device
-    B = parents.numel()
-    psrc, n = _state_of("src", src, None, Hq, Hkv, dev)
-    pdst, _ = _state_of("dst", dst, B, Hq, Hkv, dev)
-    ppar = _parents(parents, B, dev)
+    index, B = src.get_device(), parents.numel()
+    psrc, n = _state_of("src", src, 1, Hq, Hkv, index)
+    pdst, _ = _state_of("dst", dst, B, Hq, Hkv, index)
     shape = Shape(B, 1, Hq, Hkv, 64, 64, 128, OAL_BF16)
-    with _on(dev, stream) as s:
-        _check(lib().oal_state_reorder(psrc, n, ppar, pdst, ctypes.byref(shape), s),
-               "oal_state_reorder")
+    rc = lib().oal_state_reorder(psrc, n, _parents(parents, B, index), pdst, ctypes.byref(shape),
+                                 stream)
+    if rc:
+        raise OALError(rc, "oal_state_reorder")
     return dst
 
 
+@_call_on_stream
 def decay_state_reorder(src, parents, dst, stream=None):
     """oal_decay_state_reorder: dst[i] = src[parents[i]] for states [B, Hkv, 64, 64] fp32."""
-    dev = src.device
-    B, Hkv = parents.numel(), src.shape[1]
-    psrc = _need("src", src, (src.shape[0], Hkv, 64, 64), torch.float32, dev)
-    pdst = _need("dst", dst, (B, Hkv, 64, 64), torch.float32, dev)
-    ppar = _parents(parents, B, dev)
+    index, B, Hkv = src.get_device(), parents.numel(), src.shape[1]
+    psrc = _need("src", src, (src.shape[0], Hkv, 64, 64), torch.float32, index)
+    pdst = _need("dst", dst, (B, Hkv, 64, 64), torch.float32, index)
     shape = Shape(B, 1, Hkv, Hkv, 64, 64, 128, OAL_BF16)
-    with _on(dev, stream) as s:
-        _check(lib().oal_decay_state_reorder(psrc, src.shape[0], ppar, pdst, ctypes.byref(shape),
-                                             s), "oal_decay_state_reorder")
+    rc = lib().oal_decay_state_reorder(psrc, src.shape[0], _parents(parents, B, index), pdst,
+                                       ctypes.byref(shape), stream)
+    if rc:
+        raise OALError(rc, "oal_decay_state_reorder")
     return dst
 
 
+@_call_on_stream
 def decode_step_beam(q, k, v, src, parents, dst, workspace, out=None, stream=None):
     """oal_decode_step_beam: a decode step of sequence i from sequence parents[i] (int32) of the
     state buffer src, into the state buffer dst; returns out [B, Hq, 1, 64] fp32."""
-    shape = _shape_of(q, k, v, 128)
-    B, Hq, T, d = q.shape
-    Hkv, dev = shape.Hkv, q.device
-    if T != 1:
+    if q.dim() != 4 or k.dim() != 4 or q.shape[2] != 1:
         raise ValueError("decode_step_beam takes one token: q, k, v [B, H, 1, 64]")
-    pq = _need("q", q, q.shape, q.dtype, dev)
-    pk = _need("k", k, (B, Hkv, 1, d), q.dtype, dev)
-    pv = _need("v", v, (B, Hkv, 1, d), q.dtype, dev)
-    psrc, n = _state_of("src", src, None, Hq, Hkv, dev)
-    pdst, _ = _state_of("dst", dst, B, Hq, Hkv, dev)
-    ppar = _parents(parents, B, dev)
-    pw, nw = _need_ws(workspace, dev)
-    with _on(dev, stream) as s:
-        if out is None:
-            out = torch.empty(B, Hq, 1, d, dtype=torch.float32, device=dev)
-        _check(lib().oal_decode_step_beam(
-            pq, pk, pv, psrc, n, ppar, pdst,
-            _need("out", out, (B, Hq, 1, d), torch.float32, dev), pw, nw, ctypes.byref(shape), s),
-            "oal_decode_step_beam")
+    dt, index, qs = q.dtype, q.get_device(), q.shape
+    B, Hq, _, d = qs
+    Hkv = k.shape[1]
+    kv = (B, Hkv, 1, d)
+    shape = Shape(B, 1, Hq, Hkv, d, d, 128, _CODE[dt] if dt in _CODE else _dtype_code(q))
+    psrc, n = _state_of("src", src, 1, Hq, Hkv, index)
+    pdst, _ = _state_of("dst", dst, B, Hq, Hkv, index)
+    pw, nw = _need_ws(workspace, index)
+    if out is None:
+        out = torch.empty(qs, dtype=torch.float32, device=q.device)
+    rc = lib().oal_decode_step_beam(
+        _need("q", q, qs, dt, index), _need("k", k, kv, dt, index), _need("v", v, kv, dt, index),
+        psrc, n, _parents(parents, B, index), pdst, _need("out", out, qs, torch.float32, index), pw,
+        nw, ctypes.byref(shape), stream)
+    if rc:
+        raise OALError(rc, "oal_decode_step_beam")
     return out
 
 
