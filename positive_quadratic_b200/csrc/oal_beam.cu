@@ -3,14 +3,19 @@
 //
 // Selection.  A candidate (row r, token t) of a search scores running[r] + x_rt - lse_r with
 // lse_r = log sum_t exp(x_rt); the n best of the search's beams x V candidates are returned,
-// equal scores in the order of their flat place (row, then token).  Within a row the order of
-// scores is the order of logits, so no candidate outside a row's n best logits can be chosen:
-//   select_slice_kernel  one pass over the logits: each block holds a slice of a row in
-//                        registers, reduces its maximum and sum of exponentials, and lists its
-//                        n best logits;
-//   select_merge_kernel  one block per search: lse of each row from its slices, the scores of
-//                        the listed candidates in 64 bits (candidates of different rows may lie
-//                        closer than fp32 resolves), and the n best of them.
+// equal scores in the order of their flat place (row, then token).
+//   select_scan_kernel   one pass over the logits: the maximum and the sum of exponentials of
+//                        every slice, the maximum of every group of 32 logits (those that a
+//                        thread holds in registers at a time) and of every bundle of 32 groups
+//                        (a warp's);
+//   select_merge_kernel  one block per search: lse of each row; the n best bundles bound the n
+//                        best candidates from below (n different candidates reach the n-th), so
+//                        only bundles that reach it, a few n of them, have their groups looked
+//                        at; of these the n best give a better bound, and only groups that reach
+//                        it, about n, are read again and their candidates ranked.  Scores are
+//                        compared in 64 bits: candidates of different rows may lie closer than
+//                        fp32 resolves.
+// The scan is bound by memory: 6 instructions per logit, 1/32 of the logits' count written.
 #pragma once
 
 #include <cmath>
@@ -25,7 +30,11 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSelect = 32;
 constexpr int kMaxBeams = 256;
-constexpr int kList = 1024;  // survivors of the threshold that are ranked in shared memory
+constexpr int kGroup = 32;                     // logits of a group
+constexpr int kTile = kGroup * kThreads;       // logits that a block holds at a time
+constexpr int kMergeThreads = 1024;
+constexpr int kMergeWarps = kMergeThreads / 32;
+constexpr int kList = 2048;                    // candidates that are ranked in shared memory
 
 struct Slice {  // of one (row, slice)
     double sum;   // sum of exp(x - max)
@@ -33,36 +42,16 @@ struct Slice {  // of one (row, slice)
     int pad;
 };
 
-// Logits in the order of unsigned integers (-0 as 0, which it equals).
-__device__ __forceinline__ uint32_t ordered(float x)
-{
-    const uint32_t u = __float_as_uint(x + 0.f);
-    return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
-}
-__device__ __forceinline__ float unordered(uint32_t u)
-{
-    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-}
-// A logit and its place as one number: larger is better, the lower place first among equals.
-__device__ __forceinline__ unsigned long long key_of(float x, int t)
-{
-    return (static_cast<unsigned long long>(ordered(x)) << 32) | (0xFFFFFFFFu - uint32_t(t));
-}
-__device__ __forceinline__ int place_of(unsigned long long key)
-{
-    return int(0xFFFFFFFFu - uint32_t(key));
-}
-
 template <typename T> struct VecOf;
 template <> struct VecOf<float> { static constexpr int n = 4; };
 template <> struct VecOf<__nv_bfloat16> { static constexpr int n = 8; };
 
-__device__ __forceinline__ void unpack(uint4 a, float (&x)[4])
+__device__ __forceinline__ void unpack(uint4 a, float* x, float)
 {
     x[0] = __uint_as_float(a.x); x[1] = __uint_as_float(a.y);
     x[2] = __uint_as_float(a.z); x[3] = __uint_as_float(a.w);
 }
-__device__ __forceinline__ void unpack(uint4 a, float (&x)[8])
+__device__ __forceinline__ void unpack(uint4 a, float* x, __nv_bfloat16)
 {
     const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
@@ -72,149 +61,123 @@ __device__ __forceinline__ void unpack(uint4 a, float (&x)[8])
     }
 }
 
-// Block (slice, row).  Thread t holds kVecs vectors of 16 bytes, vector i at place
-// (i * 256 + t) of the slice.  A row need not start on 16 bytes: the slice starts at the
-// aligned address before it, and places outside the row count as absent.
-template <typename T, int kVecs>
-__global__ void __launch_bounds__(kThreads) select_slice_kernel(
-    const T* __restrict__ logits, long long ld, int rows, int V, int n,
-    const float* __restrict__ running, const uint8_t* __restrict__ ended,
-    unsigned long long* __restrict__ best, Slice* __restrict__ part)
+// Where a row's groups lie.  A row need not start on 16 bytes: tile 0 starts at the aligned
+// address before it, and places outside the row count as absent.  Thread t of a tile holds
+// vectors of 16 bytes number i * 256 + t; element j of its group is at place_of(t, j).  Group
+// tile * 256 + t of a row belongs to bundle (tile * 256 + t) / 32.
+template <typename T>
+__device__ __forceinline__ int place_of(int t, int j)
 {
-    constexpr int kN = VecOf<T>::n, kE = kVecs * kN;
-    const int row = blockIdx.y, slices = gridDim.x, tid = threadIdx.x, lane = tid & 31;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (ended && ended[row]) return;  // the merge does not read it
-    if (!isfinite(running[row])) return;
-    const long long first = row * ld;                 // the row's first element
-    const int skew = int(first % kN);                 // elements before it in its vector
-    const long long end = (rows - 1) * ld + V;        // of the whole array
-    const long long base = first - skew + (long long)blockIdx.x * (kE * kThreads);
-    const int t0 = int(blockIdx.x) * (kE * kThreads) - skew;  // token of the slice's place 0
-    __shared__ unsigned long long list[kList];
-    __shared__ float wmax[kWarps], wlow[kWarps];
-    __shared__ double wsum[kWarps];
-    __shared__ unsigned long long wkey[kWarps];
-    __shared__ int count;
-    if (tid == 0) count = 0;
+    constexpr int kN = VecOf<T>::n;
+    return ((j / kN) * kThreads + t) * kN + j % kN;
+}
 
-    float x[kE];
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Block (slice, row): `tiles` tiles from slice * tiles on.  gmax [rows][all tiles][256], bmax
+// [rows][all tiles][8].
+template <typename T>
+__global__ void __launch_bounds__(kThreads) select_scan_kernel(
+    const T* __restrict__ logits, long long ld, int rows, int V, int tiles, int all_tiles,
+    const float* __restrict__ running, const uint8_t* __restrict__ ended,
+    float* __restrict__ gmax, float* __restrict__ bmax, Slice* __restrict__ part)
+{
+    constexpr int kN = VecOf<T>::n, kVecs = kGroup / kN;
+    const int row = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the merge does not look at such a row's groups
+    if ((ended && ended[row]) || !isfinite(running[row])) return;
+    const long long first = row * ld;
+    const int skew = int(first % kN);
+    const long long end = (rows - 1) * ld + V;  // of the whole array
+    const int t_first = blockIdx.x * tiles, t_last = min(t_first + tiles, all_tiles);
+    float m = -INFINITY;   // this thread's maximum, and its sum of exp(x - m)
+    double s = 0.0;
+    bool nan = false;
+    uint4 raw[kVecs];
+    auto load = [&](int tile) {
+        const long long base = first - skew + (long long)tile * kTile;
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) {
-        const long long at = base + (long long)(i * kThreads + tid) * kN;
-        float v[kN];
-        if (at + kN <= end) {
-            unpack(__ldcs(reinterpret_cast<const uint4*>(logits + at)), v);
+        for (int i = 0; i < kVecs; ++i) {
+            const long long at = base + (long long)(i * kThreads + tid) * kN;
+            raw[i] = at + kN <= end ? __ldcs(reinterpret_cast<const uint4*>(logits + at))
+                                    : make_uint4(0, 0, 0, 0);
+        }
+    };
+    load(t_first);
+    for (int tile = t_first; tile < t_last; ++tile) {
+        float x[kGroup];
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i) unpack(raw[i], x + i * kN, T());
+        const int t0 = tile * kTile - skew;  // token of the tile's place 0
+        const bool edge = t0 < 0 || t0 + kTile > V;
+        if (edge) {
+            // the last vector of the array may be cut short, and tokens may lie outside the row
+            const long long base = first - skew + (long long)tile * kTile;
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) {
+                const int place = place_of<T>(tid, j);
+                if (j % kN == 0 && base + place < end && base + place + kN > end)
+                    for (int e = 0; e < kN; ++e)
+                        x[j + e] = base + place + e < end ? to_f32(logits[base + place + e]) : 0.f;
+                if (unsigned(t0 + place) >= unsigned(V)) x[j] = -INFINITY;
+            }
+        }
+        if (tile + 1 < t_last) load(tile + 1);
+        float g = x[0];
+        float chk = 0.f;
+#pragma unroll
+        for (int j = 1; j < kGroup; ++j) g = fmaxf(g, x[j]);
+        const float up = fmaxf(m, g);
+        if (up > -INFINITY) {  // (else all -inf, or NaN, which the sum below shows)
+            float p[4] = {0.f, 0.f, 0.f, 0.f};
+            // x - max first: what the largest terms lose is then next to nothing
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j) p[j & 3] += exp2_fast((x[j] - up) * kLog2e);
+            chk = (p[0] + p[1]) + (p[2] + p[3]);
+            s = (up > m && m > -INFINITY ? s * double(exp2_fast((m - up) * kLog2e)) : s) + double(chk);
+            m = up;
         } else {
 #pragma unroll
-            for (int e = 0; e < kN; ++e) v[e] = at + e < end ? to_f32(logits[at + e]) : 0.f;
+            for (int j = 0; j < kGroup; ++j) nan |= x[j] != x[j];
         }
-        const int t = t0 + (i * kThreads + tid) * kN;
+        nan |= chk != chk;
+        gmax[((long long)row * all_tiles + tile) * kThreads + tid] = g;
+        // (the order of unsigned integers is that of floats, with the sign bit turned or, for
+        // negative ones, every bit; the integer of the largest is turned back)
+        const uint32_t u = __float_as_uint(g);
+        const uint32_t top = __reduce_max_sync(~0u, u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u));
+        if (lane == 0)
+            bmax[((long long)row * all_tiles + tile) * kWarps + (tid >> 5)] =
+                __uint_as_float(top ^ ((top >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+    }
+    // the slice: sums brought to the common maximum
+    __shared__ float wmax[kWarps];
+    __shared__ double wsum[kWarps];
+    float top = m;
 #pragma unroll
-        for (int e = 0; e < kN; ++e)
-            x[i * kN + e] = (unsigned(t + e) < unsigned(V)) ? v[e] : -INFINITY;
-    }
-    auto token = [&](int i) { return t0 + ((i / kN) * kThreads + tid) * kN + i % kN; };
-
-    // the slice's maximum; a NaN stays one (fmaxf drops it, so it is looked for by itself)
-    float m = -INFINITY;
-    bool nan = false;
-#pragma unroll
-    for (int i = 0; i < kE; ++i) {
-        m = fmaxf(m, x[i]);
-        nan |= x[i] != x[i];
-    }
-    uint32_t mo = ordered(m);
-    const uint32_t wm = __reduce_max_sync(~0u, mo);
-    // a bound below which no chosen logit lies: each warp's ceil(n / 8)-th best lane maximum,
-    // and the least of those of the block's 8 warps (8 ceil(n / 8) >= n logits reach it)
-    uint32_t low = wm;
-    for (int r = (n + kWarps - 1) / kWarps; r > 1; --r) {
-        const uint32_t who = __ballot_sync(~0u, mo == low);
-        if (lane == __ffs(who) - 1) mo = 0;
-        low = __reduce_max_sync(~0u, mo);
-    }
-    if (lane == 0) {
-        wmax[tid >> 5] = unordered(wm);
-        wlow[tid >> 5] = low ? unordered(low) : -INFINITY;
-    }
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
+    if (lane == 0) wmax[tid >> 5] = top;
     nan = __syncthreads_or(nan);
-    float top = wmax[0], bound = wlow[0];
+    top = wmax[0];
 #pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-        top = fmaxf(top, wmax[w]);
-        bound = fminf(bound, wlow[w]);
-    }
-    const bool live = top > -INFINITY && top < INFINITY && !nan;
-    if (!live) {  // no finite sum: the row has no log-softmax, or this slice adds nothing to it
-        if (tid == 0) part[size_t(row) * slices + blockIdx.x] = {0.0, nan ? NAN : top, 0};
-        if (nan || top == INFINITY) return;  // the merge takes no candidate of the row
-    } else {
-        constexpr float kLog2e = 1.4426950408889634f;
-        double s = 0.0;
+    for (int w = 1; w < kWarps; ++w) top = fmaxf(top, wmax[w]);
+    double sum = m > -INFINITY && top < INFINITY ? s * double(exp2_fast((m - top) * kLog2e)) : 0.0;
 #pragma unroll
-        for (int i = 0; i < kE; i += 8) {  // fp32 sums of 8, then 64 bits
-            float p = 0.f;
-#pragma unroll
-            for (int e = i; e < i + 8; ++e) {
-                // x - top first: what the largest terms lose is then next to nothing
-                float y;
-                asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x[e] - top) * kLog2e));
-                p += y;
-            }
-            s += double(p);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-        if (lane == 0) wsum[tid >> 5] = s;
-    }
-    // every logit at or above the bound goes on the list
-#pragma unroll
-    for (int i = 0; i < kE; ++i)
-        if (x[i] >= bound && unsigned(token(i)) < unsigned(V)) {
-            const int at = atomicAdd(&count, 1);
-            if (at < kList) list[at] = key_of(x[i], token(i));
-        }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    if (lane == 0) wsum[tid >> 5] = sum;
     __syncthreads();
-    if (live && tid == 0) {
-        double s = 0.0;
-        for (int w = 0; w < kWarps; ++w) s += wsum[w];
-        part[size_t(row) * slices + blockIdx.x] = {s, top, 0};
-    }
-    unsigned long long* out = best + (size_t(row) * slices + blockIdx.x) * n;
-    const int found = count;
-    if (found <= kList) {
-        // the place of a listed logit is the number of better ones (keys are all different)
-        for (int i = tid; i < found; i += kThreads) {
-            const unsigned long long k = list[i];
-            int rank = 0;
-            for (int j = 0; j < found; ++j) rank += list[j] > k;
-            if (rank < n) out[rank] = k;
-        }
-        for (int i = found + tid; i < n; i += kThreads) out[i] = 0;  // fewer logits than n
-        return;
-    }
-    // too many equal logits at the bound: one after another, each the best below the last
-    unsigned long long last = ~0ull;
-    for (int r = 0; r < n; ++r) {
-        unsigned long long k = 0;
-#pragma unroll
-        for (int i = 0; i < kE; ++i) {
-            if (unsigned(token(i)) >= unsigned(V)) continue;
-            const unsigned long long c = key_of(x[i], token(i));
-            if (c < last && c > k) k = c;
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const unsigned long long c = __shfl_xor_sync(~0u, k, o);
-            k = c > k ? c : k;
-        }
-        if (lane == 0) wkey[tid >> 5] = k;
-        __syncthreads();
-        for (int w = 0; w < kWarps; ++w) k = wkey[w] > k ? wkey[w] : k;
-        __syncthreads();
-        if (tid == 0) out[r] = k;
-        last = k;
+    if (tid == 0) {
+        sum = 0.0;
+        for (int w = 0; w < kWarps; ++w) sum += wsum[w];
+        // (a +inf logit makes inf - inf in the sums: it is not a NaN of the row's)
+        part[(long long)row * gridDim.x + blockIdx.x] = {sum, top == INFINITY ? top : nan ? NAN : top, 0};
     }
 }
 
@@ -227,158 +190,302 @@ __device__ __forceinline__ bool better(const Candidate& a, const Candidate& b)
     return a.score > b.score || (a.score == b.score && a.place < b.place);
 }
 
-// Block = one search.  A row's candidates: its slices' lists; of an ended row the padding token
-// at its running score, and (to fill up) others at -inf; of a row without a log-softmax (a NaN
-// or +inf logit, no finite logit, a running score that is not finite) tokens at -inf.
-__global__ void __launch_bounds__(kThreads) select_merge_kernel(
-    const unsigned long long* __restrict__ best, const Slice* __restrict__ part, int beams, int V,
-    int n, int slices, const float* __restrict__ running, const uint8_t* __restrict__ ended,
-    int pad_token, float* __restrict__ scores, int32_t* __restrict__ parents,
-    int32_t* __restrict__ tokens)
+// Block = one search.  A row is live if it has a log-softmax (a finite running score and maximum,
+// no NaN).  The candidates of the others: of an ended row the padding token at its running score;
+// everything else scores -inf.
+template <typename T>
+__global__ void __launch_bounds__(kMergeThreads, 1) select_merge_kernel(
+    const T* __restrict__ logits, long long ld, const float* __restrict__ gmax,
+    const float* __restrict__ bmax, const Slice* __restrict__ part, int beams, int V, int n, int slices, int all_tiles,
+    const float* __restrict__ running, const uint8_t* __restrict__ ended, int pad_token,
+    float* __restrict__ scores, int32_t* __restrict__ parents, int32_t* __restrict__ tokens)
 {
+    constexpr int kN = VecOf<T>::n;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row0 = b * beams;
-    // of each row its largest logit and log sum exp(x - max), apart: a row of the type's lowest
-    // value would swallow the sum.  NaN: no log-softmax; not used of an ended row
-    __shared__ double lse[kMaxBeams];
+    // of each row its running score, its largest logit and log sum exp(x - max): apart, since a
+    // row of the type's lowest value would swallow the sum
+    __shared__ double shift[kMaxBeams];  // running - log sum; NaN: not live
     __shared__ float rowmax[kMaxBeams];
     __shared__ Candidate list[kList];
-    __shared__ Candidate wbest[kWarps];
-    __shared__ int count;
-    if (tid == 0) count = 0;
+    __shared__ double wlow[kMergeWarps];
+    __shared__ Candidate wbest[kMergeWarps];
+    __shared__ int groups, found;
+    __shared__ int picked[kList];
+    if (tid == 0) groups = found = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int r = warp; r < beams; r += kWarps) {
+    for (int r = warp; r < beams; r += kMergeWarps) {
         double out = NAN;
         float m = -INFINITY;
-        if (!(ended && ended[row0 + r]) && isfinite(running[row0 + r])) {
-            const Slice* p = part + size_t(row0 + r) * slices;
+        const float run = running[row0 + r];
+        if (!(ended && ended[row0 + r]) && isfinite(run)) {
+            const Slice* p = part + (long long)(row0 + r) * slices;
             bool nan = false;
             for (int i = lane; i < slices; i += 32) {
-                const float x = p[i].max;
-                nan |= x != x;
-                m = fmaxf(m, x);
+                nan |= p[i].max != p[i].max;
+                m = fmaxf(m, p[i].max);
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-            nan = __any_sync(~0u, nan);
-            if (!nan && isfinite(m)) {
+            if (!__any_sync(~0u, nan) && isfinite(m)) {
                 double s = 0.0;
                 for (int i = lane; i < slices; i += 32)
                     if (p[i].sum > 0.0) s += p[i].sum * exp(double(p[i].max) - double(m));
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-                out = log(s);
+                out = double(run) - log(s);
             }
         }
         if (lane == 0) {
-            lse[r] = out;
+            shift[r] = out;
             rowmax[r] = m;
         }
     }
     __syncthreads();
-    const int per = max(slices * n, n + 1), total = beams * per;
-    auto candidate = [&](int i) -> Candidate {
-        const int r = i / per, j = i % per;
-        const Candidate none{-INFINITY, 0x7FFFFFFFFFFFFFFFll};
-        if (ended && ended[row0 + r]) {
-            const float run = running[row0 + r];
-            if (j == 0 && unsigned(pad_token) < unsigned(V))
-                return {isfinite(run) ? double(run) : -INFINITY, (long long)r * V + pad_token};
-            const int t = j - 1;
-            if (j == 0 || t >= min(n, V) || t == pad_token) return none;
-            return {-INFINITY, (long long)r * V + t};
-        }
-        if (lse[r] != lse[r]) {
-            if (j >= min(n, V)) return none;
-            return {-INFINITY, (long long)r * V + j};
-        }
-        if (j >= slices * n) return none;
-        const unsigned long long k = best[size_t(row0 + r) * slices * n + j];
-        if (k == 0) return none;
-        const double x = double(unordered(uint32_t(k >> 32)));
-        return {double(running[row0 + r]) + ((x - double(rowmax[r])) - lse[r]),
-                (long long)r * V + place_of(k)};
+    auto score = [&](int r, float x) { return (double(x) - double(rowmax[r])) + shift[r]; };
+    const int per = all_tiles * kThreads;  // groups of a row
+    const int all_groups = beams * per;    // group i is number i % per of row i / per
+    // the group's best score; -inf where nothing is to be had
+    auto group_score = [&](int i) -> double {
+        const int r = i / per;
+        if (shift[r] != shift[r]) return -INFINITY;
+        const float x = gmax[(long long)row0 * per + i];
+        return x > -INFINITY ? score(r, x) : -INFINITY;
     };
-    auto write = [&](int rank, const Candidate& c) {
-        scores[size_t(b) * n + rank] = float(c.score);
-        parents[size_t(b) * n + rank] = row0 + int(c.place / V);
-        tokens[size_t(b) * n + rank] = int(c.place % V);
+    const int all_bundles = all_groups / 32;
+    auto bundle_score = [&](int i) -> double {
+        const int r = i / (per / 32);
+        if (shift[r] != shift[r]) return -INFINITY;
+        const float x = bmax[(long long)row0 * (per / 32) + i];
+        return x > -INFINITY ? score(r, x) : -INFINITY;
     };
-    // as in the slices: a bound that n candidates reach, the list of those that reach it, ranks
-    double m = -INFINITY;
-    for (int i = tid; i < total; i += kThreads) m = fmax(m, candidate(i).score);
-    double low = m;
-    for (int r = (n + kWarps - 1) / kWarps;; --r) {
-        low = m;
+    // Each warp's best bundle, a warp having every 32nd of them: the rows' scores differ, and a
+    // warp with one row's bundles alone would have a poor best.
+    double best = -INFINITY;
+    for (int i = 32 * lane + warp; i < all_bundles; i += kMergeThreads)
+        best = fmax(best, bundle_score(i));
+    auto warp_max = [&](double v) {
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) low = fmax(low, __shfl_xor_sync(~0u, low, o));
-        if (r == 1) break;
-        const uint32_t who = __ballot_sync(~0u, m == low);
-        if (lane == __ffs(who) - 1) m = -INFINITY;
-    }
-    if (lane == 0) wbest[warp].score = low;
+        for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(~0u, v, o));
+        return v;
+    };
+    best = warp_max(best);
+    if (lane == 0) wlow[warp] = best;
     __syncthreads();
-    double bound = wbest[0].score;
-    for (int w = 1; w < kWarps; ++w) bound = fmin(bound, wbest[w].score);
-    for (int i = tid; i < total; i += kThreads) {
-        const Candidate c = candidate(i);
-        if (c.score >= bound && c.place != 0x7FFFFFFFFFFFFFFFll) {
-            const int at = atomicAdd(&count, 1);
-            if (at < kList) list[at] = c;
+    double bound = wlow[lane];
+    // the n-th best of the 32: as many bests reach it
+    {
+        int rank = 0;
+        const double mine = bound;
+        for (int w = 0; w < 32; ++w) {
+            const double o = __shfl_sync(~0u, mine, w);
+            rank += o > mine || (o == mine && w < lane);
+        }
+        const uint32_t who = __ballot_sync(~0u, rank == n - 1);
+        bound = __shfl_sync(~0u, mine, __ffs(who) - 1);
+    }
+    // The bundles that reach the bound, the groups of theirs that do, and the n-th best of these,
+    // which is a better bound.
+    for (int i = tid; i < all_bundles; i += kMergeThreads) {
+        const double v = bundle_score(i);
+        if (v >= bound && v > -INFINITY) {
+            const int at = atomicAdd(&found, 1);
+            if (at < kList) picked[at] = i;
         }
     }
     __syncthreads();
-    const int found = count;
-    if (found <= kList) {
-        for (int i = tid; i < found; i += kThreads) {
+    for (int k = warp; k < min(found, kList); k += kMergeWarps) {
+        const int i = picked[k] * 32 + lane;
+        const double v = group_score(i);
+        if (v >= bound && v > -INFINITY) {
+            const int at = atomicAdd(&groups, 1);
+            if (at < kList) list[at] = {v, i};
+        }
+    }
+    __syncthreads();
+    int have = groups;
+    __shared__ double tighter;
+    // whether, of the groups that count, every one is listed
+    const bool all = found <= kList && have <= kList;
+    if (!all) {
+        // Many groups share the bound: the n-th best by taking one after another.
+        Candidate last{INFINITY, -1};
+        for (int k = 0; k < n; ++k) {
+            Candidate c{-INFINITY, 0x7FFFFFFFFFFFFFFFll};
+            for (int i = tid; i < all_groups; i += kMergeThreads) {
+                const Candidate x{group_score(i), i};
+                if (better(last, x) && better(x, c)) c = x;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) {
+                const Candidate x{__shfl_xor_sync(~0u, c.score, o), __shfl_xor_sync(~0u, c.place, o)};
+                if (better(x, c)) c = x;
+            }
+            if (lane == 0) wbest[warp] = c;
+            __syncthreads();
+            for (int w = 0; w < kMergeWarps; ++w)
+                if (better(wbest[w], c)) c = wbest[w];
+            __syncthreads();
+            last = c;
+        }
+        bound = last.score;
+    } else if (have > n) {
+        if (tid == 0) tighter = bound;
+        __syncthreads();
+        for (int i = tid; i < have; i += kMergeThreads) {
             const Candidate c = list[i];
             int rank = 0;
-            for (int j = 0; j < found; ++j) rank += better(list[j], c);
-            if (rank < n) write(rank, c);
+            for (int j = 0; j < have; ++j) rank += better(list[j], c);
+            if (rank == n - 1) tighter = c.score;
         }
-        return;
+        __syncthreads();
+        bound = tighter;
     }
-    Candidate last{INFINITY, -1};
-    for (int r = 0; r < n; ++r) {
-        Candidate k{-INFINITY, 0x7FFFFFFFFFFFFFFFll};
-        for (int i = tid; i < total; i += kThreads) {
-            const Candidate c = candidate(i);
-            if (better(last, c) && better(c, k)) k = c;
+    // How many groups reach the bound: about n, unless many tie.
+    __syncthreads();
+    if (tid == 0) groups = found = 0;
+    __syncthreads();
+    if (all) {
+        for (int i = tid; i < have; i += kMergeThreads)
+            if (list[i].score >= bound) picked[atomicAdd(&groups, 1)] = int(list[i].place);
+    } else {
+        for (int i = tid; i < all_groups; i += kMergeThreads) {
+            const double v = group_score(i);
+            if (v >= bound && v > -INFINITY) {
+                const int at = atomicAdd(&groups, 1);
+                if (at < kList) picked[at] = i;
+            }
         }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const Candidate c{__shfl_xor_sync(~0u, k.score, o), __shfl_xor_sync(~0u, k.place, o)};
-            if (better(c, k)) k = c;
+    }
+    __syncthreads();
+    have = groups;
+    // A group's logits, one per lane; `keep` says which count.
+    auto expand = [&](int r, int g, auto keep) {
+        const long long first = (row0 + r) * ld;
+        const int skew = int(first % kN), tile = g / kThreads;
+        const int t = tile * kTile - skew + place_of<T>(g % kThreads, lane);
+        if (unsigned(t) < unsigned(V)) {
+            const float x = to_f32(logits[first + t]);
+            const double v = x > -INFINITY ? score(r, x) : -INFINITY;
+            if (keep(v) && v > -INFINITY) {
+                const int i = atomicAdd(&found, 1);
+                if (i < kList) list[i] = {v, (long long)r * V + t};
+            }
         }
-        if (lane == 0) wbest[warp] = k;
+    };
+    const bool tied = have > (kList - kMaxBeams) / kGroup;  // more than the list is sure to hold
+    if (!tied) {
+        for (int i = warp; i < have; i += kMergeWarps)
+            expand(picked[i] / per, picked[i] % per, [&](double v) { return v >= bound; });
+    } else {
+        // Candidates above the bound are in the fewer than n groups above it.  Of those at the
+        // bound the first n in the order of their places are enough: tile by tile (places of one
+        // tile all lie before those of the next) until n are found.
+        for (int i = tid; i < all_groups; i += kMergeThreads) {  // (a multiple of 256 groups)
+            uint32_t hit = __ballot_sync(~0u, group_score(i) > bound);
+            for (; hit; hit &= hit - 1) {
+                const int g = i - lane + __ffs(hit) - 1;
+                expand(g / per, g % per, [&](double u) { return u > bound; });
+            }
+        }
         __syncthreads();
-        for (int w = 0; w < kWarps; ++w)
-            if (better(wbest[w], k)) k = wbest[w];
-        __syncthreads();
-        if (tid == 0) write(r, k);
-        last = k;
+        int ties = 0;
+        for (int r = 0; r < beams && ties < n && bound > -INFINITY; ++r)
+            for (int tile = 0; tile < all_tiles && ties < n; ++tile) {
+                const double v = tid < kThreads ? group_score(r * per + tile * kThreads + tid) : -INFINITY;
+                if (!__syncthreads_or(v >= bound)) continue;
+                // the tile's logits in the order of their places, 1024 at a time
+                const long long first = (row0 + r) * ld;
+                const int t0 = tile * kTile - int(first % kN);
+                for (int at = 0; at < kTile && ties < n; at += kMergeThreads) {
+                    const int t = t0 + at + tid;
+                    const bool hit = unsigned(t) < unsigned(V) &&
+                                     score(r, to_f32(logits[first + t])) == bound;
+                    const uint32_t in_warp = __ballot_sync(~0u, hit);
+                    __shared__ int before[kMergeWarps];
+                    if (lane == 0) before[warp] = __popc(in_warp);
+                    __syncthreads();
+                    int lower = 0, total = 0;
+                    for (int w = 0; w < kMergeWarps; ++w) {
+                        lower += w < warp ? before[w] : 0;
+                        total += before[w];
+                    }
+                    lower += __popc(in_warp & ((1u << lane) - 1));
+                    if (hit && ties + lower < n) {
+                        const int i = atomicAdd(&found, 1);
+                        if (i < kList) list[i] = {bound, (long long)r * V + t};
+                    }
+                    ties += total;
+                    __syncthreads();
+                }
+            }
+    }
+    // the padding tokens of ended rows
+    for (int r = tid; r < beams; r += kMergeThreads)
+        if (ended && ended[row0 + r] && isfinite(running[row0 + r])) {
+            const int i = atomicAdd(&found, 1);
+            if (i < kList) list[i] = {double(running[row0 + r]), (long long)r * V + pad_token};
+        }
+    __syncthreads();
+    have = found;
+    for (int i = tid; i < have; i += kMergeThreads) {
+        const Candidate c = list[i];
+        int rank = 0;
+        for (int j = 0; j < have; ++j) rank += better(list[j], c);
+        if (rank < n) {
+            scores[(long long)b * n + rank] = float(c.score);
+            parents[(long long)b * n + rank] = row0 + int(c.place / V);
+            tokens[(long long)b * n + rank] = int(c.place % V);
+        }
+    }
+    // Fewer than n candidates with a score: the rest at -inf, in the order of their places.  Of
+    // the first n + have places at most `have` are taken.
+    if (have < n && warp == 0) {
+        int rank = have;
+        for (int at = 0; rank < n; at += 32) {
+            const long long place = at + lane;
+            bool taken = false;
+            for (int j = 0; j < have; ++j) taken |= list[j].place == place;
+            const uint32_t free = __ballot_sync(~0u, !taken && place < (long long)beams * V);
+            const int mine = rank + __popc(free & ((1u << lane) - 1));
+            if (((free >> lane) & 1) && mine < n) {
+                scores[(long long)b * n + mine] = -INFINITY;
+                parents[(long long)b * n + mine] = row0 + int(place / V);
+                tokens[(long long)b * n + mine] = int(place % V);
+            }
+            rank += __popc(free);
+        }
     }
 }
 
 // ------------------------------------------------------------------------------------------
-// dst row i = src row parents[i], rows of `units` 16-byte words (a multiple of kCopy * 256 in
-// none of the uses: the last block of a row checks).  Block (part of a row, i).
+// dst row i = src row parents[i], rows of `units` 16-byte words; block (part of a row, i).  The
+// last row of blocks copies the `head` words before the rows, with the batch size of dst.
 // ------------------------------------------------------------------------------------------
 constexpr int kCopy = 8;  // words in flight per thread
 
 __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const uint4* __restrict__ src,
                                                                int src_rows,
                                                                const int32_t* __restrict__ parents,
-                                                               uint4* __restrict__ dst, int units)
+                                                               uint4* __restrict__ dst, int rows,
+                                                               int units, int head)
 {
     const int i = blockIdx.y;
+    if (i == rows) {
+        for (int e = blockIdx.x * kThreads + threadIdx.x; e < head; e += gridDim.x * kThreads) {
+            uint4 w = src[e];
+            if (e == 0) w.z = uint32_t(rows);  // StateHeader::B
+            dst[e] = w;
+        }
+        return;
+    }
     int from = parents[i];
     if (from < 0 || from >= src_rows) {
         if (threadIdx.x == 0) raise_error(OAL_ERR_VALUE);
         from = from < 0 ? 0 : src_rows - 1;
     }
-    const uint4* s = src + size_t(from) * units;
-    uint4* d = dst + size_t(i) * units;
+    const uint4* s = src + head + size_t(from) * units;
+    uint4* d = dst + head + size_t(i) * units;
     const int at = blockIdx.x * (kCopy * kThreads) + threadIdx.x;
     uint4 w[kCopy];
 #pragma unroll
@@ -388,44 +495,45 @@ __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const uint4* __re
     for (int x = 0; x < kCopy; ++x)
         if (at + x * kThreads < units) __stcs(d + at + x * kThreads, w[x]);
 }
-
-// The header (with the batch size of dst) and the coefficient tables of a state.
-__global__ void __launch_bounds__(kThreads) copy_head_kernel(const uint4* __restrict__ src,
-                                                             uint4* __restrict__ dst, int units,
-                                                             int B)
-{
-    for (int i = blockIdx.x * kThreads + threadIdx.x; i < units; i += gridDim.x * kThreads) {
-        uint4 w = src[i];
-        if (i == 0) w.z = uint32_t(B);  // StateHeader::B
-        dst[i] = w;
-    }
-}
 static_assert(offsetof(StateHeader, B) == 8, "the batch size is the header's third word");
 
 int gather_rows(const void* src, int src_rows, const int32_t* parents, void* dst, int rows,
-                size_t row_bytes, cudaStream_t st)
+                size_t row_bytes, size_t head_bytes, cudaStream_t st)
 {
-    const int units = int(row_bytes / 16);
-    const int per = kCopy * kThreads;
+    const int units = int(row_bytes / 16), per = kCopy * kThreads;
     LaunchScope ls("gather_rows", st);
-    gather_rows_kernel<<<dim3((units + per - 1) / per, rows), kThreads, 0, st>>>(
-        static_cast<const uint4*>(src), src_rows, parents, static_cast<uint4*>(dst), units);
+    gather_rows_kernel<<<dim3((units + per - 1) / per, rows + (head_bytes > 0)), kThreads, 0, st>>>(
+        static_cast<const uint4*>(src), src_rows, parents, static_cast<uint4*>(dst), rows, units,
+        int(head_bytes / 16));
     OAL_LAUNCH_CHECK();
     return OAL_OK;
 }
 
-// Slices of a row, given the logits per thread; a misaligned row needs up to a vector more.
-int slices_of(int dtype, int V, int each)
+// Tiles of a row; a misaligned row needs up to a vector more.
+int tiles_of(int dtype, int V)
 {
-    const int per = each * kThreads, skew = (dtype == OAL_BF16 ? 8 : 4) - 1;
-    return (V + skew + per - 1) / per;
+    return (V + (dtype == OAL_BF16 ? 7 : 3) + kTile - 1) / kTile;
 }
 
-// Logits per thread: 32 when that still gives every SM two blocks, else 8 (more, smaller
-// slices, so that one search's rows reach more SMs).
-int logits_per_thread(int dtype, int rows, int V)
+// Tiles per block of the scan: one, until the grid has four blocks for every SM (about as many as
+// are resident); then more, so that a block loads a tile while it works on the one before.
+int tiles_per_block(int rows, int all_tiles)
 {
-    return (long long)rows * slices_of(dtype, V, 32) >= 2 * sm_count() ? 32 : 8;
+    const long long tiles = (long long)rows * all_tiles, blocks = std::max(4 * sm_count(), 1);
+    return int(std::min<long long>(all_tiles, (tiles + blocks - 1) / blocks));
+}
+
+struct SelectLayout {
+    size_t gmax, bmax, total;  // the slices' sums lie before the maxima
+};
+SelectLayout select_layout(int dtype, int rows, int V)
+{
+    const size_t tiles = size_t(rows) * tiles_of(dtype, V);  // at least as many as slices
+    SelectLayout l;
+    l.gmax = align256(tiles * sizeof(Slice));
+    l.bmax = l.gmax + tiles * kThreads * sizeof(float);
+    l.total = l.bmax + tiles * kWarps * sizeof(float);
+    return l;
 }
 
 int check_select(int B, int beams, int V, int n, int dtype)
@@ -446,26 +554,25 @@ cudaError_t launch_select(const void* logits, long long ld, const float* running
                           cudaStream_t st)
 {
     constexpr int dtype = sizeof(T) == 2 ? OAL_BF16 : OAL_F32;
-    const int rows = B * beams, each = logits_per_thread(dtype, rows, V);
-    const int slices = slices_of(dtype, V, each);
+    const int rows = B * beams, all_tiles = tiles_of(dtype, V);
+    const int tiles = tiles_per_block(rows, all_tiles), slices = (all_tiles + tiles - 1) / tiles;
     Slice* part = static_cast<Slice*>(ws);
-    unsigned long long* best = reinterpret_cast<unsigned long long*>(
-        static_cast<unsigned char*>(ws) + align256(size_t(rows) * slices * sizeof(Slice)));
+    const SelectLayout l = select_layout(dtype, rows, V);
+    float* gmax = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + l.gmax);
+    float* bmax = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + l.bmax);
+    const T* x = static_cast<const T*>(logits);
     {
-        LaunchScope ls("select_slice", st);
-        auto go = [&](auto kern) {
-            kern<<<dim3(slices, rows), kThreads, 0, st>>>(static_cast<const T*>(logits), ld, rows,
-                                                          V, n, running, ended, best, part);
-        };
-        if (each == 32) go(select_slice_kernel<T, 32 / VecOf<T>::n>);
-        else go(select_slice_kernel<T, 8 / VecOf<T>::n>);
+        LaunchScope ls("select_scan", st);
+        select_scan_kernel<T><<<dim3(slices, rows), kThreads, 0, st>>>(
+            x, ld, rows, V, tiles, all_tiles, running, ended, gmax, bmax, part);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
     LaunchScope ls("select_merge", st);
-    return launch_ex(select_merge_kernel, dim3(B), dim3(kThreads), 0, st, true,
-                     static_cast<const unsigned long long*>(best), static_cast<const Slice*>(part),
-                     beams, V, n, slices, running, ended, pad_token, scores, parents, tokens);
+    return launch_ex(select_merge_kernel<T>, dim3(B), dim3(kMergeThreads), 0, st, true, x, ld,
+                     static_cast<const float*>(gmax), static_cast<const float*>(bmax),
+                     static_cast<const Slice*>(part), beams, V, n,
+                     slices, all_tiles, running, ended, pad_token, scores, parents, tokens);
 }
 
 int check_reorder(const void* src, int src_B, const int32_t* parents, const void* dst,
@@ -476,7 +583,7 @@ int check_reorder(const void* src, int src_B, const int32_t* parents, const void
     oal_shape from = *s;
     from.B = src_B;
     if (src_B < 1) return OAL_ERR_SHAPE;
-    if ((rc = check_common(&from)) || (rc = check_planes(s->B))) return rc;
+    if ((rc = check_common(&from)) || (rc = check_planes(s->B + 1ll))) return rc;
     if (!src || !dst || (s->B > 0 && !parents)) return OAL_ERR_NULL;
     if (!aligned16(src) || !aligned16(dst) || (reinterpret_cast<uintptr_t>(parents) & 3))
         return OAL_ERR_ALIGN;
@@ -495,9 +602,7 @@ int oal_beam_select_workspace_bytes(int B, int beams, int V, int n, int dtype, s
     const int rc = beam::check_select(B, beams, V, n, dtype);
     if (rc) return rc;
     if (!bytes) return OAL_ERR_NULL;
-    // the most slices that any launch of these sizes takes
-    const size_t parts = size_t(B) * beams * beam::slices_of(dtype, V, 8);
-    *bytes = std::max<size_t>(align256(parts * sizeof(beam::Slice)) + parts * n * 8, 256);
+    *bytes = beam::select_layout(dtype, B * beams, V).total;
     return OAL_OK;
 }
 
@@ -537,19 +642,8 @@ int oal_state_reorder(const void* src, int src_B, const int32_t* parents, void* 
     if (overlap(src, state_bytes(src_B, s->Hq, s->Hkv), dst,
                       state_bytes(s->B, s->Hq, s->Hkv)))
         return OAL_ERR_OVERLAP;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const size_t head = kHeaderBytes + coef_bytes(s->Hq);
-    {
-        LaunchScope ls("copy_state_head", st);
-        beam::copy_head_kernel<<<int((head / 16 + beam::kThreads - 1) / beam::kThreads),
-                                 beam::kThreads, 0, st>>>(
-            static_cast<const uint4*>(src), static_cast<uint4*>(dst), int(head / 16), s->B);
-        OAL_LAUNCH_CHECK();
-    }
-    if (s->B == 0) return OAL_OK;
-    return beam::gather_rows(static_cast<const unsigned char*>(src) + head, src_B, parents,
-                             static_cast<unsigned char*>(dst) + head, s->B,
-                             size_t(s->Hkv) * state_unit_bytes(), st);
+    return beam::gather_rows(src, src_B, parents, dst, s->B, size_t(s->Hkv) * state_unit_bytes(),
+                             kHeaderBytes + coef_bytes(s->Hq), static_cast<cudaStream_t>(stream));
 }
 
 int oal_decay_state_reorder(const float* src, int src_B, const int32_t* parents, float* dst,
@@ -560,7 +654,7 @@ int oal_decay_state_reorder(const float* src, int src_B, const int32_t* parents,
     const size_t row = size_t(s->Hkv) * kD * kDV * 4;
     if (overlap(src, src_B * row, dst, s->B * row)) return OAL_ERR_OVERLAP;
     if (s->B == 0) return OAL_OK;
-    return beam::gather_rows(src, src_B, parents, dst, s->B, row,
+    return beam::gather_rows(src, src_B, parents, dst, s->B, row, 0,
                              static_cast<cudaStream_t>(stream));
 }
 
