@@ -14,30 +14,43 @@ constexpr int kC = 64;          // tokens per chunk of the fp32 kernels
 constexpr int kThreads = 256;
 constexpr int kLd = kD + 4;     // padded row: 16-byte reads of 8 consecutive rows touch all banks
 
-// Rows [t0, t0 + n) of head plane `src` into a [64][kLd] tile, zero from row n on.
-__device__ __forceinline__ void load_tile(float (*dst)[kLd], const float* src, int t0, int n,
-                                          const float* row_scale = nullptr)
+// Starts copying rows [t0, t0 + n) of head plane `src` into a [64][kLd] tile; zeros from row n on.
+__device__ __forceinline__ void fetch_tile(float (*dst)[kLd], const float* src, int t0, int n)
 {
-    for (int e = threadIdx.x; e < kC * kD / 4; e += kThreads) {
-        const int r = e / (kD / 4), c = 4 * (e % (kD / 4));
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (r < n) {
-            a = *reinterpret_cast<const float4*>(src + size_t(t0 + r) * kD + c);
-            if (row_scale) {
-                const float w = row_scale[r];
-                a = make_float4(a.x * w, a.y * w, a.z * w, a.w * w);
-            }
-        }
-        *reinterpret_cast<float4*>(&dst[r][c]) = a;
+#pragma unroll
+    for (int i = 0; i < kC * kD / 4 / kThreads; ++i) {
+        const int e = i * kThreads + threadIdx.x, r = e / (kD / 4), c = 4 * (e % (kD / 4));
+        const float* from = src + size_t(t0 + min(r, n - 1)) * kD + c;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(&dst[r][c])),
+                     "l"(from), "r"(r < n ? 16 : 0)
+                     : "memory");
     }
 }
+__device__ __forceinline__ void fetch_end() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void fetch_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+__device__ __forceinline__ float2 lo2(float4 v) { return make_float2(v.x, v.y); }
+__device__ __forceinline__ float2 hi2(float4 v) { return make_float2(v.z, v.w); }
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // ------------------------------------------------------------------------------------------
 // E_c of one (chunk, kv, b): a 64 x 64 product over the chunk's tokens, for every y head of the
-// kv head.  Thread (ty, tx) owns rows 4 ty .. + 3 and columns 4 tx .. + 3.
+// kv head.  Thread (ty, tx) owns rows 4 ty .. + 3 and columns 4 tx .. + 3, in pairs of columns
+// (packed fp32 FMAs); the next head's tiles arrive while one is worked on.
 // ------------------------------------------------------------------------------------------
+struct DeltaSmem {
+    float Y[2][kC][kLd], Z[2][kC][kLd];
+    float w[kC];
+};
+
 __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, DecaySum a, DecaySum b2)
 {
+    extern __shared__ __align__(16) unsigned char smem_raw[];
+    DeltaSmem& sm = *reinterpret_cast<DeltaSmem*>(smem_raw);
     const DecaySum& J = blockIdx.z ? b2 : a;
     const int c = blockIdx.x, bkv = blockIdx.y, b = bkv / S.Hkv, kv = bkv % S.Hkv;
     tc::grid_dep_launch();
@@ -50,36 +63,48 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
                                 make_float4(0.f, 0.f, 0.f, 0.f));
         return;
     }
-    __shared__ __align__(16) float Y[kC][kLd], Z[kC][kLd];
-    __shared__ float w[kC];
+    const int grp = J.hy / S.Hkv;
+    const size_t plane = (size_t(b) * J.hy + kv * grp) * S.T * kD, next = size_t(S.T) * kD;
+    auto fetch = [&](int h) {
+        fetch_tile(sm.Y[h & 1], static_cast<const float*>(J.y) + plane + h * next, c * kC, n);
+        fetch_tile(sm.Z[h & 1], static_cast<const float*>(J.z) + plane + h * next, c * kC, n);
+        fetch_end();
+    };
+    fetch(0);
     const float g = decay_log(S.log_decay, kv);
     if (threadIdx.x < kC)
-        w[threadIdx.x] = J.rev ? S.scale * decay_pow(g, threadIdx.x + 1)
-                               : decay_pow(g, max(0, n - 1 - int(threadIdx.x)));
-    const int grp = J.hy / S.Hkv;
-    float acc[4][4] = {};
+        sm.w[threadIdx.x] = J.rev ? S.scale * decay_pow(g, threadIdx.x + 1)
+                                  : decay_pow(g, max(0, n - 1 - int(threadIdx.x)));
+    float2 acc[4][2] = {};
     for (int h = 0; h < grp; ++h) {
-        const size_t plane = (size_t(b) * J.hy + kv * grp + h) * S.T * kD;
+        if (h + 1 < grp) {
+            fetch(h + 1);
+            fetch_wait<1>();
+        } else {
+            fetch_wait<0>();
+        }
         __syncthreads();
-        load_tile(Y, static_cast<const float*>(J.y) + plane, c * kC, n, w);
-        load_tile(Z, static_cast<const float*>(J.z) + plane, c * kC, n);
-        __syncthreads();
+        const float (*Y)[kLd] = sm.Y[h & 1];
+        const float (*Z)[kLd] = sm.Z[h & 1];
 #pragma unroll 4
         for (int j = 0; j < kC; ++j) {
+            const float w = sm.w[j];
             const float4 y = *reinterpret_cast<const float4*>(&Y[j][4 * ty]);
             const float4 z = *reinterpret_cast<const float4*>(&Z[j][4 * tx]);
-            const float yv[4] = {y.x, y.y, y.z, y.w}, zv[4] = {z.x, z.y, z.z, z.w};
+            const float yv[4] = {y.x * w, y.y * w, y.z * w, y.w * w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][e] = fmaf(yv[i], zv[e], acc[i][e]);
+            for (int i = 0; i < 4; ++i) {
+                acc[i][0] = __ffma2_rn(both(yv[i]), lo2(z), acc[i][0]);
+                acc[i][1] = __ffma2_rn(both(yv[i]), hi2(z), acc[i][1]);
+            }
         }
+        __syncthreads();
     }
     float* out = J.delta + (size_t(bkv) * S.chunks + c) * kDecayState;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int e = (4 * ty + i) * kDV + 4 * tx;
-        const float4 sum = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+        const float4 sum = make_float4(acc[i][0].x, acc[i][0].y, acc[i][1].x, acc[i][1].y);
         if (S.chunks > 1) *reinterpret_cast<float4*>(out + e) = sum;
         else scan_one<float>(J, bkv, e, decay_pow(g, n), sum);
     }
@@ -88,7 +113,7 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
 // ------------------------------------------------------------------------------------------
 // The scan over the chunks of every (b, kv): cur <- l^n cur + E_c, cur written before each.
 // Block = 64 state entries (two per lane) and up to 64 chunks at a time, 8 per warp: a warp sums
-// its 8 chunks by themselves, all of them loaded at once, then starts over from what the warps
+// its chunks by themselves, all of them loaded at once, then starts over from what the warps
 // before it leave.  One round trip to memory for 64 chunks instead of 64.
 // ------------------------------------------------------------------------------------------
 constexpr int kScanCols = 64, kScanRun = 8;
@@ -124,8 +149,9 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(DecayShape S, DecaySum a
     float2 cur = make_float2(0.f, 0.f);
     if (J.first)
         cur = *reinterpret_cast<const float2*>(J.first + size_t(bkv) * kDecayState + e);
-    for (int base = 0; base < nc; base += 8 * kScanRun) {
-        const int i0 = base + warp * kScanRun, cnt = max(0, min(kScanRun, nc - i0));
+    const int run = min(kScanRun, (nc + 7) / 8);  // chunks per warp at a time
+    for (int base = 0; base < nc; base += 8 * run) {
+        const int i0 = base + warp * run, cnt = max(0, min(run, nc - i0));
         auto chunk_at = [&](int i) { return J.rev ? nc - 1 - (i0 + i) : i0 + i; };
         auto decay_at = [&](int i) { return chunk_at(i) == nc - 1 ? l_tail : l_full; };
         float2 d[kScanRun];
@@ -173,16 +199,68 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(DecayShape S, DecaySum a
 }
 
 // ------------------------------------------------------------------------------------------
-// The mix of one (chunk, x head, b).  Thread (ty, tx) owns rows 4 ty .. + 3; of the scores the
-// columns tx + 16 e (conflict-free reads of y rows), of the output the columns 4 tx .. + 3.
+// The mix of one (chunk, x head, b).  Thread (ty, tx) owns rows 4 ty .. + 3; of products of rows
+// (x . y) the columns tx + 16 e (conflict-free reads of y rows), of the output the columns
+// 4 tx .. + 3.  Packed fp32 FMAs; tiles arrive while others are worked on.
 // ------------------------------------------------------------------------------------------
 struct MixSmem {
-    float X[kC][kLd], Y[kC][kLd], Z[kC][kLd], P[kC][kLd];
+    float X[kC][kLd], Y[kC][kLd], Z[kC][kLd], M[kC][kLd], P[kC][kLd];
     float pw[kC + 1];  // powers of l
 };
 
-__global__ void __launch_bounds__(kThreads) mix_simt_kernel(DecayShape S, DecayJob j0, DecayJob j1,
-                                                            DecayJob j2)
+// s[i][e] = A[4 ty + i] . B[tx + 16 e]
+__device__ __forceinline__ void row_products(const float (*A)[kLd], const float (*B)[kLd],
+                                             float (&s)[4][4])
+{
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    float2 acc[4][4] = {};
+#pragma unroll 4
+    for (int k = 0; k < kD; k += 4) {
+        float4 a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = *reinterpret_cast<const float4*>(&A[4 * ty + i][k]);
+            b[i] = *reinterpret_cast<const float4*>(&B[tx + 16 * i][k]);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                acc[i][e] = __ffma2_rn(lo2(a[i]), lo2(b[e]), acc[i][e]);
+                acc[i][e] = __ffma2_rn(hi2(a[i]), hi2(b[e]), acc[i][e]);
+            }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][e] = acc[i][e].x + acc[i][e].y;
+}
+
+// acc[i] += row 4 ty + i of A times B, columns 4 tx .. + 3
+__device__ __forceinline__ void add_product(const float (*A)[kLd], const float (*B)[kLd],
+                                            float2 (&acc)[4][2])
+{
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+#pragma unroll 4
+    for (int k = 0; k < kC; k += 4) {
+        float4 a[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(&A[4 * ty + i][k]);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+            const float4 b = *reinterpret_cast<const float4*>(&B[k + kk][4 * tx]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float v = kk == 0 ? a[i].x : kk == 1 ? a[i].y : kk == 2 ? a[i].z : a[i].w;
+                acc[i][0] = __ffma2_rn(both(v), lo2(b), acc[i][0]);
+                acc[i][1] = __ffma2_rn(both(v), hi2(b), acc[i][1]);
+            }
+        }
+    }
+}
+
+__global__ void __launch_bounds__(kThreads, 2) mix_simt_kernel(DecayShape S, DecayJob j0, DecayJob j1,
+                                                               DecayJob j2)
 {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     MixSmem& sm = *reinterpret_cast<MixSmem*>(smem_raw);
@@ -197,69 +275,28 @@ __global__ void __launch_bounds__(kThreads) mix_simt_kernel(DecayShape S, DecayJ
     const int kv = hx * S.Hkv / J.hx;
     const int nh = J.hy > J.hx ? J.hy / J.hx : 1;
     const int y0 = J.hy > J.hx ? hx * nh : hx * J.hy / J.hx;
-    const float g = decay_log(S.log_decay, kv);
-    for (int e = threadIdx.x; e <= kC; e += kThreads) sm.pw[e] = decay_pow(g, e);
+    const size_t next = size_t(S.T) * kD, plane = (size_t(b) * J.hy + y0) * next;
+    const float* y = static_cast<const float*>(J.y) + plane;
+    const float* z = static_cast<const float*>(J.z) + plane;
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    load_tile(sm.X, static_cast<const float*>(J.x) + (size_t(b) * J.hx + hx) * S.T * kD, c * kC, n);
+    // the inputs were there before the kernels whose results this one waits for
+    fetch_tile(sm.X, static_cast<const float*>(J.x) + (size_t(b) * J.hx + hx) * next, c * kC, n);
+    fetch_tile(sm.Y, y, c * kC, n);
+    fetch_end();
+    fetch_tile(sm.Z, z, c * kC, n);
+    const float g = decay_log(S.log_decay, kv);
+    if (threadIdx.x <= kC) sm.pw[threadIdx.x] = decay_pow(g, threadIdx.x);
     tc::grid_dep_wait();
-    // M (or its transpose) where Z goes later
-    const float* M = static_cast<const float*>(J.mem) +
-                     ((size_t(b) * S.Hkv + kv) * S.chunks + c) * kDecayState;
-    for (int e = threadIdx.x; e < kDecayState; e += kThreads) {
-        const int r = e / kDV, cc = e % kDV;
-        if (J.mem_t) sm.Z[cc][r] = M[e];
-        else sm.Z[r][cc] = M[e];
-    }
+    fetch_tile(sm.M,
+               static_cast<const float*>(J.mem) + ((size_t(b) * S.Hkv + kv) * S.chunks + c) * kDecayState,
+               0, kC);
+    fetch_end();
+    fetch_wait<1>();
     __syncthreads();
-    auto product = [&](const float (*A)[kLd], const float (*Bm)[kLd], float (&acc)[4][4]) {
-#pragma unroll 2
-        for (int k = 0; k < kC; k += 4) {
-            float av[4][4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float4 t4 = *reinterpret_cast<const float4*>(&A[4 * ty + i][k]);
-                av[i][0] = t4.x; av[i][1] = t4.y; av[i][2] = t4.z; av[i][3] = t4.w;
-            }
-#pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-                const float4 b4 = *reinterpret_cast<const float4*>(&Bm[k + kk][4 * tx]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    acc[i][0] = fmaf(av[i][kk], b4.x, acc[i][0]);
-                    acc[i][1] = fmaf(av[i][kk], b4.y, acc[i][1]);
-                    acc[i][2] = fmaf(av[i][kk], b4.z, acc[i][2]);
-                    acc[i][3] = fmaf(av[i][kk], b4.w, acc[i][3]);
-                }
-            }
-        }
-    };
-    float far[4][4] = {}, near[4][4] = {};
-    product(sm.X, sm.Z, far);
+    float2 near[4][2] = {};
     for (int h = 0; h < nh; ++h) {
-        const size_t plane = (size_t(b) * J.hy + y0 + h) * S.T * kD;
-        __syncthreads();
-        load_tile(sm.Y, static_cast<const float*>(J.y) + plane, c * kC, n);
-        load_tile(sm.Z, static_cast<const float*>(J.z) + plane, c * kC, n);
-        __syncthreads();
-        float s[4][4] = {};
-#pragma unroll 2
-        for (int k = 0; k < kD; k += 4) {
-            float4 x4[4], y4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x4[i] = *reinterpret_cast<const float4*>(&sm.X[4 * ty + i][k]);
-                y4[i] = *reinterpret_cast<const float4*>(&sm.Y[tx + 16 * i][k]);
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[i][e] = fmaf(x4[i].x, y4[e].x, s[i][e]);
-                    s[i][e] = fmaf(x4[i].y, y4[e].y, s[i][e]);
-                    s[i][e] = fmaf(x4[i].z, y4[e].z, s[i][e]);
-                    s[i][e] = fmaf(x4[i].w, y4[e].w, s[i][e]);
-                }
-        }
+        float s[4][4];
+        row_products(sm.X, sm.Y, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -268,8 +305,38 @@ __global__ void __launch_bounds__(kThreads) mix_simt_kernel(DecayShape S, DecayJ
                 const int d = J.rev ? col - row : row - col;
                 sm.P[row][col] = d >= 0 ? s[i][e] * sm.pw[d] : 0.f;
             }
+        fetch_wait<0>();
+        __syncthreads();  // P and Z (and M) are there, Y is free
+        if (h + 1 < nh) {
+            fetch_tile(sm.Y, y + (h + 1) * next, c * kC, n);
+            fetch_end();
+        }
+        add_product(sm.P, sm.Z, near);
+        if (h + 1 < nh) {
+            fetch_wait<0>();
+            __syncthreads();  // the next Y is there, Z and P are free
+            fetch_tile(sm.Z, z + (h + 1) * next, c * kC, n);
+            fetch_end();
+        }
+    }
+    float2 far[4][2] = {};
+    if (J.mem_t) {
+        float s[4][4];
+        row_products(sm.X, sm.M, s);
+        __syncthreads();  // P is free
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sm.P[4 * ty + i][tx + 16 * e] = s[i][e];
         __syncthreads();
-        product(sm.P, sm.Z, near);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 v = *reinterpret_cast<const float4*>(&sm.P[4 * ty + i][4 * tx]);
+            far[i][0] = lo2(v);
+            far[i][1] = hi2(v);
+        }
+    } else {
+        add_product(sm.X, sm.M, far);
     }
     float* out = static_cast<float*>(J.out) + ((size_t(b) * J.hx + hx) * S.T + c * kC) * kD;
 #pragma unroll
@@ -278,8 +345,8 @@ __global__ void __launch_bounds__(kThreads) mix_simt_kernel(DecayShape S, DecayJ
         if (row >= n) continue;
         const float bi = J.rev ? sm.pw[n - 1 - row] : S.scale * sm.pw[row + 1];
         *reinterpret_cast<float4*>(out + size_t(row) * kD + 4 * tx) = make_float4(
-            fmaf(S.scale, near[i][0], bi * far[i][0]), fmaf(S.scale, near[i][1], bi * far[i][1]),
-            fmaf(S.scale, near[i][2], bi * far[i][2]), fmaf(S.scale, near[i][3], bi * far[i][3]));
+            fmaf(S.scale, near[i][0].x, bi * far[i][0].x), fmaf(S.scale, near[i][0].y, bi * far[i][0].y),
+            fmaf(S.scale, near[i][1].x, bi * far[i][1].x), fmaf(S.scale, near[i][1].y, bi * far[i][1].y));
     }
 }
 
@@ -409,6 +476,7 @@ cudaError_t set_attributes_once()
     const std::pair<const void*, int> smem[] = {
         {reinterpret_cast<const void*>(dtc::delta_kernel), int(dtc::kDeltaSmem)},
         {reinterpret_cast<const void*>(dtc::mix_kernel), int(dtc::kMixSmem)},
+        {reinterpret_cast<const void*>(delta_simt_kernel), int(sizeof(DeltaSmem))},
         {reinterpret_cast<const void*>(mix_simt_kernel), int(sizeof(MixSmem))}};
     for (const auto& k : smem) {
         if ((e = cudaFuncSetAttribute(k.first, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -468,7 +536,8 @@ int launch_sums(const DecayShape& S, const DecaySum* a, int n, const oal_shape* 
             }
             dtc::delta_kernel<<<items, dtc::kThreads, dtc::kDeltaSmem, st>>>(maps, S, a[0], b2);
         } else {
-            delta_simt_kernel<<<dim3(S.chunks, planes, n), kThreads, 0, st>>>(S, a[0], b2);
+            delta_simt_kernel<<<dim3(S.chunks, planes, n), kThreads, sizeof(DeltaSmem), st>>>(S, a[0],
+                                                                                             b2);
         }
         OAL_LAUNCH_CHECK();
     }
