@@ -628,6 +628,7 @@ def _call_on_stream(f):
     makes belong to that stream, and their memory is not handed out again before the call's
     kernels are done with it."""
     first = f.__code__.co_varnames[0]
+    device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
     @functools.wraps(f)
     def call(*args, stream=None, **kwargs):
@@ -635,10 +636,10 @@ def _call_on_stream(f):
         index = x.get_device()
         if index < 0:
             raise ValueError("tensors must be contiguous CUDA tensors")
-        if stream is None and index == torch._C._cuda_getDevice():
-            return f(*args, stream=torch._C._cuda_getCurrentRawStream(index), **kwargs)
+        if stream is None and index == device():
+            return f(*args, stream=raw(index), **kwargs)
         with _There(x.device, stream):
-            return f(*args, stream=torch._C._cuda_getCurrentRawStream(index), **kwargs)
+            return f(*args, stream=raw(index), **kwargs)
     return call
 
 
@@ -663,19 +664,37 @@ def _need_ws(ws, index):
 _CODE = {torch.bfloat16: OAL_BF16, torch.float32: OAL_F32}
 
 
+_F32 = torch.float32
+
+
+def _same(index, dt, *ts):
+    """Whether the tensors are contiguous, of type dt and on CUDA device `index`: one pass over
+    what a call's arguments have in common (a call of one token takes a few microseconds)."""
+    for t in ts:
+        if t.dtype is not dt or t.get_device() != index or not t.is_contiguous():
+            return False
+    return True
+
+
 def _decay_args(q, k, v, log_decay, lens):
     """(shape, sizes, the pointers of q, k, v, log_decay, lens) of a decayed linear attention
     call; sizes: of q, of k and v, of the state."""
-    if q.dim() != 4 or k.dim() != 4:
+    qs, kv = q.shape, k.shape
+    if len(qs) != 4 or len(kv) != 4:
         raise ValueError("q, k, v must be [B, H, T, 64]")
-    dt, index, qs = q.dtype, q.get_device(), q.shape
+    dt, index = q.dtype, q.get_device()
     B, Hq, T, d = qs
-    Hkv = k.shape[1]
-    kv = (B, Hkv, T, d)
+    Hkv = kv[1]
+    if not (_same(index, dt, q, k, v) and kv == v.shape and kv == (B, Hkv, T, d) and
+            log_decay.shape == (Hkv,) and _same(index, _F32, log_decay)):
+        kv = (B, Hkv, T, d)
+        _need("q", q, qs, dt, index)
+        _need("k", k, kv, dt, index)
+        _need("v", v, kv, dt, index)
+        _need("log_decay", log_decay, (Hkv,), _F32, index)
     shape = Shape(B, T, Hq, Hkv, d, d, 128, _CODE[dt] if dt in _CODE else _dtype_code(q))
     return shape, (qs, kv, (B, Hkv, 64, 64), dt, index), (
-        _need("q", q, qs, dt, index), _need("k", k, kv, dt, index), _need("v", v, kv, dt, index),
-        _need("log_decay", log_decay, (Hkv,), torch.float32, index),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), log_decay.data_ptr(),
         None if lens is None else _need("lens", lens, (B,), torch.int32, index))
 
 
@@ -707,8 +726,10 @@ def _decay_prefill(name, q, k, v, log_decay, scale, lens, out, state, want_out, 
             out = torch.empty_like(q) if lens is None else torch.zeros_like(q)
         po = _need("out", out, qs, dt, index)
     if state is None:
-        state = torch.empty(ss, dtype=torch.float32, device=q.device)
-    ps = _need("state", state, ss, torch.float32, index)
+        state = q.new_empty(ss, dtype=_F32)
+        ps = state.data_ptr()
+    else:
+        ps = _need("state", state, ss, _F32, index)
     if workspace is None:
         workspace = empty_workspace(_bytes_of("oal_decay_prefill_workspace_bytes", shape), q.device)
     pw, nw = _need_ws(workspace, index)
@@ -759,8 +780,11 @@ def decay_step(q, k, v, log_decay, scale: float, state, src=None, parents=None, 
         ppar = _parents(parents, qs[0], index)
     if out is None:
         out = torch.empty_like(q)
-    rc = lib().oal_decay_step(pq, pk, pv, pg, scale, psrc, n, ppar, ps,
-                              _need("out", out, qs, dt, index), ctypes.byref(shape), stream)
+        po = out.data_ptr()
+    else:
+        po = _need("out", out, qs, dt, index)
+    rc = lib().oal_decay_step(pq, pk, pv, pg, scale, psrc, n, ppar, ps, po, ctypes.byref(shape),
+                              stream)
     if rc:
         raise OALError(rc, "oal_decay_step")
     return out
@@ -837,23 +861,24 @@ def beam_select(logits, running, n: int, ended=None, pad_token: int = 0, scores=
     dt = logits.dtype
     code = _CODE[dt] if dt in _CODE else _dtype_code(logits)
     rows, best, i32 = (B, beams), (B, n), torch.int32
-    if scores is None:
-        scores = torch.empty(best, dtype=torch.float32, device=logits.device)
-    if parents is None and tokens is None:
-        parents, tokens = torch.empty((2, B, n), dtype=i32, device=logits.device).unbind(0)
-    elif parents is None:
-        parents = torch.empty(best, dtype=i32, device=logits.device)
-    elif tokens is None:
-        tokens = torch.empty(best, dtype=i32, device=logits.device)
+    if scores is None and parents is None and tokens is None:
+        parents, tokens, scores = running.new_empty((3, B, n), dtype=i32).unbind(0)
+        scores = scores.view(_F32)
+        ps, pp, pt = scores.data_ptr(), parents.data_ptr(), tokens.data_ptr()
+    else:
+        scores = running.new_empty(best, dtype=_F32) if scores is None else scores
+        parents = running.new_empty(best, dtype=i32) if parents is None else parents
+        tokens = running.new_empty(best, dtype=i32) if tokens is None else tokens
+        ps, pp, pt = (_need("scores", scores, best, _F32, index),
+                      _need("parents", parents, best, i32, index),
+                      _need("tokens", tokens, best, i32, index))
     if workspace is None:
         workspace = empty_workspace(_select_bytes(B, beams, V, n, code), logits.device)
     pw, nw = _need_ws(workspace, index)
     rc = lib().oal_beam_select(
-        logits.data_ptr(), ld, code, _need("running", running, rows, torch.float32, index),
+        logits.data_ptr(), ld, code, _need("running", running, rows, _F32, index),
         None if ended is None else _need("ended", ended, rows, torch.uint8, index), pad_token, B,
-        beams, V, n, _need("scores", scores, best, torch.float32, index),
-        _need("parents", parents, best, i32, index), _need("tokens", tokens, best, i32, index), pw,
-        nw, stream)
+        beams, V, n, ps, pp, pt, pw, nw, stream)
     if rc:
         raise OALError(rc, "oal_beam_select")
     return scores, parents, tokens
@@ -866,8 +891,7 @@ def _state_of(name, t, B, Hq, Hkv, index):
     if t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor on cuda:{index}")
     # the layout of oal_state_bytes: header and coefficient tables, then the sequences
-    held = (t.numel() - 256 - (Hq * FEATURES_PAD * 4 + 255) // 256 * 256) // (
-        Hkv * FEATURES_PAD * (VALUE_DIM + 1) * 4)
+    held = (t.numel() - 256 - Hq * FEATURES_PAD * 4) // (Hkv * FEATURES_PAD * (VALUE_DIM + 1) * 4)
     if held < B:
         raise ValueError(f"{name} holds {t.numel()} bytes, too few for its sequences")
     return t.data_ptr(), held
@@ -917,11 +941,13 @@ def decode_step_beam(q, k, v, src, parents, dst, workspace, out=None, stream=Non
     pdst, _ = _state_of("dst", dst, B, Hq, Hkv, index)
     pw, nw = _need_ws(workspace, index)
     if out is None:
-        out = torch.empty(qs, dtype=torch.float32, device=q.device)
+        out = q.new_empty(qs, dtype=_F32)
+        po = out.data_ptr()
+    else:
+        po = _need("out", out, qs, _F32, index)
     rc = lib().oal_decode_step_beam(
         _need("q", q, qs, dt, index), _need("k", k, kv, dt, index), _need("v", v, kv, dt, index),
-        psrc, n, _parents(parents, B, index), pdst, _need("out", out, qs, torch.float32, index), pw,
-        nw, ctypes.byref(shape), stream)
+        psrc, n, _parents(parents, B, index), pdst, po, pw, nw, ctypes.byref(shape), stream)
     if rc:
         raise OALError(rc, "oal_decode_step_beam")
     return out
