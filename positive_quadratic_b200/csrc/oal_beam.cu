@@ -35,6 +35,7 @@ constexpr int kTile = kGroup * kThreads;       // logits that a block holds at a
 constexpr int kMergeThreads = 1024;
 constexpr int kMergeWarps = kMergeThreads / 32;
 constexpr int kList = 2048;                    // candidates that are ranked in shared memory
+constexpr int kFew = (kList - kMaxBeams) / kGroup;  // groups whose logits the list is sure to hold
 
 struct Slice {  // of one (row, slice)
     double sum;   // sum of exp(x - max)
@@ -70,6 +71,17 @@ __device__ __forceinline__ int place_of(int t, int j)
 {
     constexpr int kN = VecOf<T>::n;
     return ((j / kN) * kThreads + t) * kN + j % kN;
+}
+
+// Floats in the order of unsigned integers, and back.
+__device__ __forceinline__ uint32_t ordered(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u)
+{
+    return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -149,13 +161,9 @@ __global__ void __launch_bounds__(kThreads) select_scan_kernel(
         }
         nan |= chk != chk;
         gmax[((long long)row * all_tiles + tile) * kThreads + tid] = g;
-        // (the order of unsigned integers is that of floats, with the sign bit turned or, for
-        // negative ones, every bit; the integer of the largest is turned back)
-        const uint32_t u = __float_as_uint(g);
-        const uint32_t top = __reduce_max_sync(~0u, u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u));
+        const uint32_t best = __reduce_max_sync(~0u, ordered(g));
         if (lane == 0)
-            bmax[((long long)row * all_tiles + tile) * kWarps + (tid >> 5)] =
-                __uint_as_float(top ^ ((top >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+            bmax[((long long)row * all_tiles + tile) * kWarps + (tid >> 5)] = unordered(best);
     }
     // the slice: sums brought to the common maximum
     __shared__ float wmax[kWarps];
@@ -208,7 +216,7 @@ __global__ void __launch_bounds__(kMergeThreads, 1) select_merge_kernel(
     __shared__ double shift[kMaxBeams];  // running - log sum; NaN: not live
     __shared__ float rowmax[kMaxBeams];
     __shared__ Candidate list[kList];
-    __shared__ double wlow[kMergeWarps];
+    __shared__ uint32_t wlow[kMergeWarps];
     __shared__ Candidate wbest[kMergeWarps];
     __shared__ int groups, found;
     __shared__ int picked[kList];
@@ -260,29 +268,26 @@ __global__ void __launch_bounds__(kMergeThreads, 1) select_merge_kernel(
         return x > -INFINITY ? score(r, x) : -INFINITY;
     };
     // Each warp's best bundle, a warp having every 32nd of them: the rows' scores differ, and a
-    // warp with one row's bundles alone would have a poor best.
+    // warp with one row's bundles alone would have a poor best.  The bound is the n-th best of the
+    // warps' bests, which n <= 32 bundles reach; rounded down to fp32, where a warp's maximum is
+    // one instruction.
     double best = -INFINITY;
     for (int i = 32 * lane + warp; i < all_bundles; i += kMergeThreads)
         best = fmax(best, bundle_score(i));
-    auto warp_max = [&](double v) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(~0u, v, o));
-        return v;
-    };
-    best = warp_max(best);
-    if (lane == 0) wlow[warp] = best;
+    const uint32_t warp_best = __reduce_max_sync(~0u, ordered(__double2float_rd(best)));
+    if (lane == 0) wlow[warp] = warp_best;
     __syncthreads();
-    double bound = wlow[lane];
-    // the n-th best of the 32: as many bests reach it
+    double bound;
     {
+        const uint32_t mine = wlow[lane];
         int rank = 0;
-        const double mine = bound;
+#pragma unroll
         for (int w = 0; w < 32; ++w) {
-            const double o = __shfl_sync(~0u, mine, w);
+            const uint32_t o = wlow[w];
             rank += o > mine || (o == mine && w < lane);
         }
         const uint32_t who = __ballot_sync(~0u, rank == n - 1);
-        bound = __shfl_sync(~0u, mine, __ffs(who) - 1);
+        bound = unordered(__shfl_sync(~0u, mine, __ffs(who) - 1));
     }
     // The bundles that reach the bound, the groups of theirs that do, and the n-th best of these,
     // which is a better bound.
@@ -329,7 +334,7 @@ __global__ void __launch_bounds__(kMergeThreads, 1) select_merge_kernel(
             last = c;
         }
         bound = last.score;
-    } else if (have > n) {
+    } else if (have > kFew) {
         if (tid == 0) tighter = bound;
         __syncthreads();
         for (int i = tid; i < have; i += kMergeThreads) {
@@ -341,7 +346,7 @@ __global__ void __launch_bounds__(kMergeThreads, 1) select_merge_kernel(
         __syncthreads();
         bound = tighter;
     }
-    // How many groups reach the bound: about n, unless many tie.
+    // The groups that reach the bound: few, unless many tie.
     __syncthreads();
     if (tid == 0) groups = found = 0;
     __syncthreads();
@@ -373,7 +378,7 @@ __global__ void __launch_bounds__(kMergeThreads, 1) select_merge_kernel(
             }
         }
     };
-    const bool tied = have > (kList - kMaxBeams) / kGroup;  // more than the list is sure to hold
+    const bool tied = have > kFew;
     if (!tied) {
         for (int i = warp; i < have; i += kMergeWarps)
             expand(picked[i] / per, picked[i] % per, [&](double v) { return v >= bound; });

@@ -318,7 +318,7 @@ constexpr int kInfos = 4;  // items that the look-ahead warp may have described 
 // What the other warps need to know of an item, and the powers of l in either order, so that a row's
 // factors are read in the order of its keys: l^i at up[kPw0 + i], l^(127 - i) at down[kPw0 + i].  Pairs
 // that start at an odd place are 8-byte aligned; the factors of a diagonal block's other side lie up
-// to 31 places before the first power (up) or behind the last (down) and are not used.
+// to 31 places before the first power (up) or behind the last (down), where zeros are.
 constexpr int kPw0 = 33;
 struct MixInfo {
     __nv_bfloat16* out;    // the tile's first row
@@ -467,13 +467,8 @@ struct MixWalk {
 __device__ __forceinline__ void decay_scores(uint32_t scores, const MixInfo& I, int qw, int jb,
                                              int lane)
 {
-    const int rev = I.rev, left = I.n - 32 * jb;
-    // keys that count: this side of the diagonal, and not behind the sequence's end (which matters
-    // where rows look at later keys)
-    const uint32_t before = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1;
-    uint32_t live = rev ? before : ~0u;
+    const int rev = I.rev;
     const int ahead = rev ? jb - qw : qw - jb;  // blocks between the rows and the keys
-    if (ahead == 0) live &= rev ? ~0u << lane : ~0u >> (31 - lane);
     uint32_t p[16];
     if (ahead < 0) {
 #pragma unroll
@@ -500,8 +495,12 @@ __device__ __forceinline__ void decay_scores(uint32_t scores, const MixInfo& I, 
                 s[x + 1] = v.y;
             }
         }
-        if (__any_sync(~0u, live != ~0u)) {
-            // chosen, not multiplied by zero: what is not live may be NaN
+        if (I.garbage) {
+            // keys behind the sequence's end may be anything: their products are chosen to be zero,
+            // as multiplied by zero they might be NaN
+            const int left = I.n - 32 * jb;
+            uint32_t live = left >= 32 ? ~0u : left <= 0 ? 0u : (1u << left) - 1;
+            if (ahead == 0) live &= rev ? ~0u << lane : ~0u >> (31 - lane);
 #pragma unroll
             for (int x = 0; x < 32; ++x) s[x] = (live >> x) & 1 ? s[x] : 0.f;
         }
@@ -677,6 +676,8 @@ __global__ void __launch_bounds__(kMixThreads, 2)
             const int gi = at.gi;
             at.advance(jobs, S, lane);
             const bool last = !shares || gi + 1 == grp || !at.more();
+            I.up[kPw0 - 32 + lane] = 0.f;
+            if (lane < 31) I.down[kPw0 + kC + lane] = 0.f;
 #pragma unroll 1
             for (int i = 0; i < kC; i += 32) {
                 const float l = decay_pow(g, i + lane);
