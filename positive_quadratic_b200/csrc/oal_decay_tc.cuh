@@ -87,25 +87,26 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int n)
 // bf16 operand: it is split into three bf16 parts (8 + 8 + 8 digits, all of an fp32 product), and
 // the state keeps fp32 accuracy.  Rows of the accumulator: [hi; mid] in one MMA group of M = 128
 // and [lo; hi] in a second, of which lo is used, so that E = hi + (mid + lo).
-// One CTA per (sum, part of the heads, b, kv, chunk); two fit an SM.
+// One CTA per (sum, part of the heads, b, kv, chunk); three fit an SM, since the high part is written
+// over y itself.
 // ------------------------------------------------------------------------------------------
 struct SumMaps {
     CUtensorMap y[2], z[2];
 };
 
 struct DeltaCtl {
-    uint64_t y_full, z_full[2], parts, done;
+    uint64_t full, parts, done;
     uint32_t tmem_base;
     int abort_flag;
 };
 
-constexpr uint32_t kDOffY = 0, kDOffZ = kTile, kDOffLo = 3 * kTile, kDOffHi = 4 * kTile;
-constexpr uint32_t kDOffCtl = 6 * kTile;
+constexpr uint32_t kDOffLo = 0, kDOffY = kTile, kDOffZ = 3 * kTile;  // lo | y, then hi | mid | z
+constexpr uint32_t kDOffCtl = 4 * kTile;
 constexpr uint32_t kDeltaSmem = kDOffCtl + 128 + 1024;
 constexpr uint32_t kDeltaTmem = 128;
-static_assert(sizeof(DeltaCtl) <= 128 && 2 * (kDeltaSmem + 1024) <= 233472, "two CTAs per SM");
+static_assert(sizeof(DeltaCtl) <= 128 && 3 * (kDeltaSmem + 1024) <= 233472, "three CTAs per SM");
 
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
     delta_kernel(const __grid_constant__ SumMaps maps, DecayShape S, DecaySum a, DecaySum b2)
 {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -132,9 +133,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         tmem_relinquish();
     }
     if (threadIdx.x == 0) {
-        mbar_init(&ctl.y_full, 1);
-        mbar_init(&ctl.z_full[0], 1);
-        mbar_init(&ctl.z_full[1], 1);
+        mbar_init(&ctl.full, 1);
         mbar_init(&ctl.parts, 8);
         mbar_init(&ctl.done, 1);
         ctl.abort_flag = 0;
@@ -156,9 +155,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const uint32_t lo = smem_u32(sm + kDOffLo);
             bool ok = true;
             for (int i = 0; i < nh; ++i) {
-                ok = wait_warp(&ctl.y_full, i & 1, abort_flag) &&
-                     wait_warp(&ctl.z_full[i & 1], (i >> 1) & 1, abort_flag) &&
-                     (i == 0 || wait_warp(&ctl.done, (i - 1) & 1, abort_flag));
+                ok = wait_warp(&ctl.full, i & 1, abort_flag);
                 if (!ok) break;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
@@ -181,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                     sts128(lo + 2 * kTile + off, p[1][0], p[1][1], p[1][2], p[1][3]);
                     sts128(lo + off, p[2][0], p[2][1], p[2][2], p[2][3]);
                 }
-                if (n < kC) zero_rows<256>(sm + kDOffZ + (i & 1) * kTile, n);
+                if (n < kC) zero_rows<256>(sm + kDOffZ, n);
                 fence_proxy_async();
                 warp_arrive(&ctl.parts);
             }
@@ -232,46 +229,35 @@ __global__ void __launch_bounds__(kThreads, 2)
             const CUtensorMap* mz = &maps.z[which];
             const int plane = b * J.hy + kv * grp + h0;
             const uint32_t lo = smem_u32(sm + kDOffLo), z = smem_u32(sm + kDOffZ);
-            int ny = 0, nz = 0, nmma = 0;
-            auto load_y = [&](int i) {
-                mbar_expect_tx(&ctl.y_full, kTile);
-                tma_load_3d(sm + kDOffY, my, &ctl.y_full, 0, c * kC, plane + i);
-                ++ny;
+            int loads = 0, products = 0;
+            auto load = [&](int i) {
+                mbar_expect_tx(&ctl.full, 2 * kTile);
+                tma_load_3d(sm + kDOffY, my, &ctl.full, 0, c * kC, plane + i);
+                tma_load_3d(sm + kDOffZ, mz, &ctl.full, 0, c * kC, plane + i);
+                ++loads;
             };
-            auto load_z = [&](int i) {
-                mbar_expect_tx(&ctl.z_full[i & 1], kTile);
-                tma_load_3d(sm + kDOffZ + (i & 1) * kTile, mz, &ctl.z_full[i & 1], 0, c * kC,
-                            plane + i);
-                ++nz;
-            };
-            load_y(0);
-            load_z(0);
-            if (nh > 1) load_z(1);
+            load(0);
             for (int i = 0; i < nh; ++i) {
                 if (!wait(&ctl.parts, i & 1, abort_flag)) break;
-                if (i + 1 < nh) load_y(i + 1);  // the parts of head i have been formed
                 tc_fence_after();
-                const uint32_t zi = z + (i & 1) * kTile;
 #pragma unroll
                 for (int g = 0; g < 2; ++g)
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         mma_bf16(tmem + 64 * g,
                                  sdesc_sw128(lo + (1 - g) * kTile + ks * 2048, kTile, 1024),
-                                 sdesc_sw128(zi + ks * 2048, kTile, 1024), id,
+                                 sdesc_sw128(z + ks * 2048, kTile, 1024), id,
                                  (i > 0 || ks > 0) ? 1u : 0u);
                 mma_commit(&ctl.done);
-                ++nmma;
-                if (i + 2 < nh) {
+                ++products;
+                if (i + 1 < nh) {
                     if (!wait(&ctl.done, i & 1, abort_flag)) break;
-                    load_z(i + 2);
+                    load(i + 1);
                 }
             }
             // nothing of this CTA is in flight when it ends
-            bounded_spin_done(&ctl.y_full, (ny - 1) & 1);
-            bounded_spin_done(&ctl.z_full[(nz - 1) & 1], ((nz - 1) >> 1) & 1);
-            if (nz > 1) bounded_spin_done(&ctl.z_full[nz & 1], ((nz - 2) >> 1) & 1);
-            if (nmma) bounded_spin_done(&ctl.done, (nmma - 1) & 1);
+            bounded_spin_done(&ctl.full, (loads - 1) & 1);
+            if (products) bounded_spin_done(&ctl.done, (products - 1) & 1);
         }
     }
     if (n <= 0 && S.chunks == 1 && warp < 8)
