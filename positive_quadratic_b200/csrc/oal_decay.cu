@@ -112,31 +112,55 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
 
 // ------------------------------------------------------------------------------------------
 // The scan over the chunks of every (b, kv): cur <- l^n cur + E_c, cur written before each.
-// Block = 64 state entries (two per lane) and up to 64 chunks at a time, 8 per warp: a warp sums
-// its chunks by themselves, all of them loaded at once, then starts over from what the warps
-// before it leave.  One round trip to memory for 64 chunks instead of 64.
+// Block = 32 kVec state entries (kVec per lane) and up to 64 chunks at a time, 8 per warp: a warp
+// sums its chunks by themselves, all of them loaded at once, then starts over from what the warps
+// before it leave.  One round trip to memory for 64 chunks instead of 64.  kVec = 2 gives twice
+// the blocks of kVec = 4, which matters where there are few planes.
 // ------------------------------------------------------------------------------------------
-constexpr int kScanCols = 64, kScanRun = 8;
+constexpr int kScanRun = 8;
 
-__device__ __forceinline__ void store2(float* p, float2 v) { *reinterpret_cast<float2*>(p) = v; }
-__device__ __forceinline__ void store2(__nv_bfloat16* p, float2 v)
+template <int kVec> struct Entries {
+    float v[kVec];
+};
+template <int kVec>
+__device__ __forceinline__ Entries<kVec> load_entries(const float* p)
 {
-    *reinterpret_cast<uint32_t*>(p) = tc::pack_bf16x2(v.x, v.y);
+    Entries<kVec> e;
+    if constexpr (kVec == 4)
+        *reinterpret_cast<float4*>(e.v) = *reinterpret_cast<const float4*>(p);
+    else
+        *reinterpret_cast<float2*>(e.v) = *reinterpret_cast<const float2*>(p);
+    return e;
 }
-__device__ __forceinline__ float2 fma_decay(float l, float2 cur, float2 d)
+__device__ __forceinline__ void store_entries(float* p, const Entries<2>& e)
 {
-    return make_float2(fmaf(l, cur.x, d.x), fmaf(l, cur.y, d.y));
+    *reinterpret_cast<float2*>(p) = make_float2(e.v[0], e.v[1]);
 }
-
+__device__ __forceinline__ void store_entries(__nv_bfloat16* p, const Entries<2>& e)
+{
+    *reinterpret_cast<uint32_t*>(p) = tc::pack_bf16x2(e.v[0], e.v[1]);
+}
 template <typename Tm>
+__device__ __forceinline__ void store_entries(Tm* p, const Entries<4>& e)
+{
+    store_state(p, make_float4(e.v[0], e.v[1], e.v[2], e.v[3]));
+}
+template <int kVec>
+__device__ __forceinline__ void fma_decay(float l, Entries<kVec>& cur, const Entries<kVec>& d)
+{
+#pragma unroll
+    for (int x = 0; x < kVec; ++x) cur.v[x] = fmaf(l, cur.v[x], d.v[x]);
+}
+
+template <typename Tm, int kVec>
 __global__ void __launch_bounds__(kThreads) scan_kernel(DecayShape S, DecaySum a, DecaySum b2,
                                                         int chunk)
 {
     const DecaySum& J = blockIdx.z ? b2 : a;
     const int bkv = blockIdx.y, b = bkv / S.Hkv, kv = bkv % S.Hkv;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int e = blockIdx.x * kScanCols + 2 * lane;
-    __shared__ float2 tot[8][32];
+    const int e = (blockIdx.x * 32 + lane) * kVec;
+    __shared__ Entries<kVec> tot[8][32];
     __shared__ float pw[8];
     tc::grid_dep_launch();
     const int len = decay_len(S, b);
@@ -145,57 +169,53 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(DecayShape S, DecaySum a
     const float l_full = decay_pow(g, chunk), l_tail = decay_pow(g, tail);
     const size_t plane = (size_t(bkv) * S.chunks) * kDecayState + e;
     const size_t part = size_t(S.B) * S.Hkv * S.chunks * kDecayState;
-    tc::grid_dep_wait();
-    float2 cur = make_float2(0.f, 0.f);
-    if (J.first)
-        cur = *reinterpret_cast<const float2*>(J.first + size_t(bkv) * kDecayState + e);
     const int run = min(kScanRun, (nc + 7) / 8);  // chunks per warp at a time
+    tc::grid_dep_wait();
+    Entries<kVec> cur{};
+    if (J.first) cur = load_entries<kVec>(J.first + size_t(bkv) * kDecayState + e);
     for (int base = 0; base < nc; base += 8 * run) {
         const int i0 = base + warp * run, cnt = max(0, min(run, nc - i0));
         auto chunk_at = [&](int i) { return J.rev ? nc - 1 - (i0 + i) : i0 + i; };
         auto decay_at = [&](int i) { return chunk_at(i) == nc - 1 ? l_tail : l_full; };
-        float2 d[kScanRun];
+        Entries<kVec> d[kScanRun];
 #pragma unroll
         for (int i = 0; i < kScanRun; ++i)
-            if (i < cnt)
-                d[i] = *reinterpret_cast<const float2*>(J.delta + plane +
-                                                        size_t(chunk_at(i)) * kDecayState);
+            if (i < cnt) d[i] = load_entries<kVec>(J.delta + plane + size_t(chunk_at(i)) * kDecayState);
         for (int p = 1; p < J.parts; ++p) {
 #pragma unroll
             for (int i = 0; i < kScanRun; ++i)
                 if (i < cnt) {
-                    const float2 x = *reinterpret_cast<const float2*>(
-                        J.delta + p * part + plane + size_t(chunk_at(i)) * kDecayState);
-                    d[i].x += x.x;
-                    d[i].y += x.y;
+                    const Entries<kVec> x = load_entries<kVec>(J.delta + p * part + plane +
+                                                               size_t(chunk_at(i)) * kDecayState);
+                    fma_decay(1.f, d[i], x);
                 }
         }
-        float2 sum = make_float2(0.f, 0.f);
+        Entries<kVec> sum{};
         int tokens = 0;
 #pragma unroll
         for (int i = 0; i < kScanRun; ++i)
             if (i < cnt) {
-                sum = fma_decay(decay_at(i), sum, d[i]);
+                fma_decay(decay_at(i), sum, d[i]);
                 tokens += chunk_at(i) == nc - 1 ? tail : chunk;
             }
         tot[warp][lane] = sum;
         if (lane == 0) pw[warp] = decay_pow(g, tokens);
         __syncthreads();
-        float2 mine = cur;
+        Entries<kVec> mine = cur;
 #pragma unroll
         for (int w = 0; w < 8; ++w) {
             if (w == warp) mine = cur;
-            cur = fma_decay(pw[w], cur, tot[w][lane]);
+            fma_decay(pw[w], cur, tot[w][lane]);
         }
 #pragma unroll
         for (int i = 0; i < kScanRun; ++i)
             if (i < cnt) {
-                store2(static_cast<Tm*>(J.mem) + plane + size_t(chunk_at(i)) * kDecayState, mine);
-                mine = fma_decay(decay_at(i), mine, d[i]);
+                store_entries(static_cast<Tm*>(J.mem) + plane + size_t(chunk_at(i)) * kDecayState, mine);
+                fma_decay(decay_at(i), mine, d[i]);
             }
         __syncthreads();
     }
-    if (J.last && warp == 0) store2(J.last + size_t(bkv) * kDecayState + e, cur);
+    if (J.last && warp == 0) store_entries(J.last + size_t(bkv) * kDecayState + e, cur);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -543,8 +563,10 @@ int launch_sums(const DecayShape& S, const DecaySum* a, int n, const oal_shape* 
     }
     if (S.chunks == 1) return OAL_OK;  // there is nothing to scan
     LaunchScope ls("decay_scan", st);
-    OAL_CUDA_TRY(launch_ex(on_tensor_cores(s) ? scan_kernel<__nv_bfloat16> : scan_kernel<float>,
-                           dim3(kDecayState / kScanCols, planes, n), dim3(kThreads), 0, st,
+    const bool wide = n * planes >= 8;
+    const auto scan = on_tensor_cores(s) ? (wide ? scan_kernel<__nv_bfloat16, 4> : scan_kernel<__nv_bfloat16, 2>)
+                                         : (wide ? scan_kernel<float, 4> : scan_kernel<float, 2>);
+    OAL_CUDA_TRY(launch_ex(scan, dim3(kDecayState / (wide ? 128 : 64), planes, n), dim3(kThreads), 0, st,
                            S.chunks > 0, S, a[0], b2, chunk_of(s)));
     return OAL_OK;
 }
