@@ -301,18 +301,20 @@ constexpr int kMixThreads = (kMixWarps + 2) * 32;
 constexpr int kMmaWarp = kMixWarps, kAheadWarp = kMixWarps + 1;
 constexpr int kInfos = 4;  // items that the look-ahead warp may have described and not seen done
 
-// What the other warps need to know of an item, and the powers of l in either order, so that a row's
-// factors are read in the order of its keys: l^i at up[kPw0 + i], l^(127 - i) at down[kPw0 + i].  Pairs
-// that start at an odd place are 8-byte aligned; the factors of a diagonal block's other side lie up
-// to 31 places before the first power (up) or behind the last (down), where zeros are.
-constexpr int kPw0 = 33;
+// What the other warps need to know of an item, and a table of powers of l: entry kT0 + j is l^j
+// (rev) or l^(127 - j), so that a row's factors l^|i-j| are read in the order of its keys whatever
+// the direction; zeros follow where the other side of the diagonal begins.  Two copies, the second
+// shifted by one place: rows at even and odd places both read aligned pairs (and, 16 banks apart,
+// without conflicts).
+constexpr int kT0 = 32, kTab = 208;
+static_assert(kTab % 32 == 16, "the copies lie 16 banks apart");
 struct MixInfo {
     __nv_bfloat16* out;    // the tile's first row
     const CUtensorMap* o;  // of the output; NULL: rows behind the sequence's end are not to be written
     int n, nh, rev, has_m, mem_t, t0, plane, garbage, none;
     int fresh, last;  // first, last item of a run that shares Y, Z and M
     int pad;
-    float up[kPw0 + kC + 1], down[kPw0 + kC + 31];
+    float tab[2][kTab];
 };
 
 struct MixCtl {
@@ -335,9 +337,7 @@ constexpr uint32_t kMixTmem = 256;
 constexpr uint32_t kColS = 0, kColU = 128, kColF = 192;
 static_assert(sizeof(MixCtl) <= 256 && kMOffCtl % 8 == 0 && 2 * (kMixSmem + 1024) <= 233472,
               "two CTAs per SM");
-static_assert(sizeof(MixInfo) % 8 == 0 && offsetof(MixInfo, up) % 8 == 0 &&
-                  offsetof(MixInfo, down) % 8 == 0 && kPw0 % 2 == 1,
-              "alignment of the powers");
+static_assert(sizeof(MixInfo) % 8 == 0 && offsetof(MixInfo, tab) % 8 == 0, "alignment of the table");
 static_assert(kMixWarps * 2048 <= kTile, "output staging");
 
 // A CTA's place in the work: item `i` of job w, at (b, chunk c, kv, head gi of the group).  Held by
@@ -462,24 +462,15 @@ __device__ __forceinline__ void decay_scores(uint32_t scores, const MixInfo& I, 
     } else {
         float s[32];
         tmem_ld32(scores, s);
-        if (ahead == 0) {
-            const float* d = rev ? I.up + kPw0 - lane : I.down + kPw0 + 127 - lane;
-            tmem_ld_wait();
+        const int at = kT0 - lane + (rev ? 32 * ahead : 127 - 32 * ahead);
+        const float* d = I.tab[at & 1] + at + (at & 1);
+        tmem_ld_wait();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) s[x] *= d[x];
-        } else {
-            // l^|i-j| = l^(from the row to its block's edge) l^(from there to j)
-            const float rf = I.up[kPw0 + (rev ? 31 - lane : lane)];
-            const float* d = rev ? I.up + kPw0 + 32 * ahead - 31 : I.down + kPw0 + 127 - 32 * ahead;
-            const float2 rf2 = make_float2(rf, rf);
-            tmem_ld_wait();
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-                const float2 v = __fmul2_rn(make_float2(s[x], s[x + 1]),
-                                            __fmul2_rn(rf2, *reinterpret_cast<const float2*>(d + x)));
-                s[x] = v.x;
-                s[x + 1] = v.y;
-            }
+        for (int x = 0; x < 32; x += 2) {
+            const float2 v = __fmul2_rn(make_float2(s[x], s[x + 1]),
+                                        *reinterpret_cast<const float2*>(d + x));
+            s[x] = v.x;
+            s[x + 1] = v.y;
         }
         if (I.garbage) {
             // keys behind the sequence's end may be anything: their products are chosen to be zero,
@@ -572,8 +563,8 @@ __global__ void __launch_bounds__(kMixThreads, 2)
                 warp_arrive(&ctl.p_full);
             }
             if (!ok) break;
-            const float bi = rev ? (row < n ? I.up[kPw0 + n - 1 - row] : 0.f)
-                                 : S.scale * I.up[kPw0 + row + 1];
+            const float bi = rev ? (row < n ? I.tab[0][kT0 + n - 1 - row] : 0.f)
+                                 : S.scale * I.tab[0][kT0 + 126 - row];
             __nv_bfloat16* out = I.out + row * kD + 32 * kh;
             const CUtensorMap* o = I.o;
             const int t0 = I.t0 + 32 * qw, plane = I.plane;
@@ -591,7 +582,13 @@ __global__ void __launch_bounds__(kMixThreads, 2)
                 tmem_ld32(lanes + kColF + 32 * kh, f);
                 tmem_ld_wait();
 #pragma unroll
-                for (int x = 0; x < 32; ++x) u[x] = fmaf(bi, f[x], S.scale * u[x]);
+                for (int x = 0; x < 32; x += 2) {
+                    const float2 v = __ffma2_rn(make_float2(bi, bi), make_float2(f[x], f[x + 1]),
+                                                __fmul2_rn(make_float2(S.scale, S.scale),
+                                                           make_float2(u[x], u[x + 1])));
+                    u[x] = v.x;
+                    u[x + 1] = v.y;
+                }
             } else {
                 tmem_ld_wait();
 #pragma unroll
@@ -662,16 +659,14 @@ __global__ void __launch_bounds__(kMixThreads, 2)
             const int gi = at.gi;
             at.advance(jobs, S, lane);
             const bool last = !shares || gi + 1 == grp || !at.more();
-            I.up[kPw0 - 32 + lane] = 0.f;
-            if (lane < 31) I.down[kPw0 + kC + lane] = 0.f;
 #pragma unroll 1
-            for (int i = 0; i < kC; i += 32) {
-                const float l = decay_pow(g, i + lane);
-                I.up[kPw0 + i + lane] = l;
-                I.down[kPw0 + 127 - i - lane] = l;
+            for (int e = lane; e < 6 * 32; e += 32) {
+                const int m = J.j.rev ? e - kT0 : 127 - (e - kT0);
+                const float l = m >= 0 && m <= kC ? decay_pow(g, m) : 0.f;
+                I.tab[0][e] = l;
+                I.tab[1][e + 1] = l;
             }
             if (lane == 0) {
-                I.up[kPw0 + kC] = decay_pow(g, kC);
                 I.out = static_cast<__nv_bfloat16*>(J.j.out) + (size_t(plane) * S.T + c * kC) * kD;
                 I.o = n == min(kC, left) ? &J.o : nullptr;
                 I.t0 = c * kC;

@@ -472,8 +472,9 @@ constexpr int kDecWarps = kDecThreads / 32;
 // kBeam: sequence b continues the state of sequence parents[b] of `src` (a beam search's
 // reordering), and the whole result (sums, padding rows, coefficients) goes to `state`, which
 // holds nothing before.  The sums are read and written once either way, so the reordering by
-// itself, another read and write of them, is saved; several beams of one parent read it from L2
-// (the loads are not marked for eviction).
+// itself, another read and write of them, is saved.  Beams of one parent lie side by side in the
+// grid and read it from L2 even though the loads are marked for early eviction, as in the step in
+// place (64 beams of 14/2 heads: 32.2 us, against 34.6 us with ordinary loads).
 template <typename Tin, int kGrp, bool kBeam>  // kGrp = Hq / Hkv query heads per kv head
 __global__ void __launch_bounds__(kDecThreads, 4) decode_kernel(const Tin* __restrict__ q,
                                                               const Tin* __restrict__ k,
@@ -507,7 +508,6 @@ __global__ void __launch_bounds__(kDecThreads, 4) decode_kernel(const Tin* __res
     }
     const float* Hv_in = unit_in;
     const float* z_in = unit_in + size_t(kFP) * kDV;
-    auto load4 = [](const float4* p) { return kBeam ? __ldg(p) : __ldcs(p); };
 
     __shared__ __align__(16) float vh[kW + 3];
     __shared__ float kh[kDA];
@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kDecThreads, 4) decode_kernel(const Tin* __res
     for (int x = 0; x < kDecBatch; ++x) {
         const int row = rsub + kRowStep * x;
         if (row < nrows)
-            hv[x] = load4(reinterpret_cast<const float4*>(Hv_in + size_t(f0 + row) * kDV) + lane4);
+            hv[x] = __ldcs(reinterpret_cast<const float4*>(Hv_in + size_t(f0 + row) * kDV) + lane4);
     }
 
     // this thread's row of the slab (kDecRows < kDecThreads: at most one): its readout
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(kDecThreads, 4) decode_kernel(const Tin* __res
         for (int x = 0; x < kDecBatch; ++x) {
             const int row = base + kRowStep * (kDecBatch + x);
             if (row < nrows)
-                nx[x] = load4(reinterpret_cast<const float4*>(Hv_in + size_t(f0 + row) * kDV) + lane4);
+                nx[x] = __ldcs(reinterpret_cast<const float4*>(Hv_in + size_t(f0 + row) * kDV) + lane4);
         }
 #pragma unroll
         for (int x = 0; x < kDecBatch; ++x) {

@@ -934,8 +934,13 @@ def decode_step_beam(q, k, v, src, parents, dst, workspace, out=None, stream=Non
         raise ValueError("decode_step_beam takes one token: q, k, v [B, H, 1, 64]")
     dt, index, qs = q.dtype, q.get_device(), q.shape
     B, Hq, _, d = qs
-    Hkv = k.shape[1]
-    kv = (B, Hkv, 1, d)
+    kv = k.shape
+    Hkv = kv[1]
+    if not (_same(index, dt, q, k, v) and kv == v.shape and kv == (B, Hkv, 1, d)):
+        kv = (B, Hkv, 1, d)
+        _need("q", q, qs, dt, index)
+        _need("k", k, kv, dt, index)
+        _need("v", v, kv, dt, index)
     shape = Shape(B, 1, Hq, Hkv, d, d, 128, _CODE[dt] if dt in _CODE else _dtype_code(q))
     psrc, n = _state_of("src", src, 1, Hq, Hkv, index)
     pdst, _ = _state_of("dst", dst, B, Hq, Hkv, index)
@@ -946,8 +951,8 @@ def decode_step_beam(q, k, v, src, parents, dst, workspace, out=None, stream=Non
     else:
         po = _need("out", out, qs, _F32, index)
     rc = lib().oal_decode_step_beam(
-        _need("q", q, qs, dt, index), _need("k", k, kv, dt, index), _need("v", v, kv, dt, index),
-        psrc, n, _parents(parents, B, index), pdst, po, pw, nw, ctypes.byref(shape), stream)
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), psrc, n, _parents(parents, B, index), pdst, po, pw,
+        nw, ctypes.byref(shape), stream)
     if rc:
         raise OALError(rc, "oal_decode_step_beam")
     return out
