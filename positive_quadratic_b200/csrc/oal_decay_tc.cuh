@@ -63,6 +63,38 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32])
     for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
+// MMAs from descriptors whose low words are at hand (the high word is the same for every tile here).
+// One thread issues them all, at a few cycles an instruction, and the chain from one item to the next
+// goes through it: forming each descriptor from an address again took it longer than the products.
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);  // see tc::sdesc_sw128
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr, uint32_t lbo)
+{
+    return ((saddr >> 4) & 0x3FFFu) | ((lbo >> 4) << 16);
+}
+template <bool kAdd>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 a, {%1, %3};\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "n"(int(kAdd))
+        : "memory");
+}
+template <bool kAdd>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "n"(int(kAdd))
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16])
 {
     asm volatile(
@@ -241,13 +273,14 @@ __global__ void __launch_bounds__(kThreads, 3)
                 if (!wait(&ctl.parts, i & 1, abort_flag)) break;
                 tc_fence_after();
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
+                for (int g = 0; g < 2; ++g) {
+                    const uint32_t a_lo = desc_lo(lo + (1 - g) * kTile, kTile), b_lo = desc_lo(z, kTile);
+                    if (i > 0) mma_ss<true>(tmem + 64 * g, a_lo, b_lo, id);
+                    else mma_ss<false>(tmem + 64 * g, a_lo, b_lo, id);
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        mma_bf16(tmem + 64 * g,
-                                 sdesc_sw128(lo + (1 - g) * kTile + ks * 2048, kTile, 1024),
-                                 sdesc_sw128(z + ks * 2048, kTile, 1024), id,
-                                 (i > 0 || ks > 0) ? 1u : 0u);
+                    for (int ks = 1; ks < 8; ++ks)
+                        mma_ss<true>(tmem + 64 * g, a_lo + 128 * ks, b_lo + 128 * ks, id);
+                }
                 mma_commit(&ctl.done);
                 ++products;
                 if (i + 1 < nh) {
@@ -733,7 +766,11 @@ __global__ void __launch_bounds__(kMixThreads, 2)
     } else if (lane == 0) {
         constexpr uint32_t id_s = idesc_bf16(128, 128, false, false);
         constexpr uint32_t id_mn = idesc_bf16(128, 64, false, true), id_k = idesc_bf16(128, 64, false, false);
-        const uint32_t m = smem_u32(sm + kMOffM);
+        // low words of the descriptors; the other buffer's is kTile / 16 further on
+        const uint32_t x0 = desc_lo(smem_u32(sm + kMOffX), 16);
+        const uint32_t y0 = desc_lo(smem_u32(sm + kMOffYZ), 16);
+        const uint32_t z0 = desc_lo(smem_u32(sm + kMOffYZ + kTile), kTile);
+        const uint32_t m0 = desc_lo(smem_u32(sm + kMOffM), kTile);
         int nm = 0, step = 0, tile = -1;
         bool ok = true;
         // Every wait and every commit of this thread costs a few hundred cycles of the chain from
@@ -759,7 +796,7 @@ __global__ void __launch_bounds__(kMixThreads, 2)
             if (!ok || it.none) break;
             const Next now = it;
             ready = false;
-            const uint32_t x = smem_u32(sm + kMOffX + (done & 1) * kTile);
+            const uint32_t x = x0 + (done & 1) * (kTile / 16);
             for (int h = 0; ok && h < now.nh; ++h, ++step) {
                 if (h > 0 || now.first) {
                     ++tile;
@@ -770,11 +807,11 @@ __global__ void __launch_bounds__(kMixThreads, 2)
                 else if (ok && done > 0)
                     ok = wait(&ctl.item_done[(done - 1) & 1], ((done - 1) >> 1) & 1, abort_flag);
                 if (!ok) break;
-                const uint32_t y = smem_u32(sm + kMOffYZ) + (tile & 1) * 2 * kTile, z = y + kTile;
-#pragma unroll 1
-                for (int ks = 0; ks < 4; ++ks)
-                    mma_bf16(tmem + kColS, sdesc_sw128(x + ks * 32, 16, 1024),
-                             sdesc_sw128(y + ks * 32, 16, 1024), id_s, ks > 0 ? 1u : 0u);
+                const uint32_t y = y0 + (tile & 1) * (2 * kTile / 16);
+                const uint32_t z = z0 + (tile & 1) * (2 * kTile / 16);
+                mma_ss<false>(tmem + kColS, x, y, id_s);
+#pragma unroll
+                for (int ks = 1; ks < 4; ++ks) mma_ss<true>(tmem + kColS, x + 2 * ks, y + 2 * ks, id_s);
                 mma_commit(&ctl.s_full);
                 if (h == 0 && now.has_m && now.first) {
                     ok = wait(&ctl.m_full, nm & 1, abort_flag);
@@ -789,17 +826,17 @@ __global__ void __launch_bounds__(kMixThreads, 2)
                 ok = wait(&ctl.p_full, step & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int ks = 0; ks < 8; ++ks)
-                    mma_bf16_ts(tmem + kColU, tmem + kColS + 32 * (ks >> 1) + 8 * (ks & 1),
-                                sdesc_sw128(z + ks * 2048, kTile, 1024), id_mn,
-                                (h > 0 || ks > 0) ? 1u : 0u);
+                if (h > 0) mma_ts<true>(tmem + kColU, tmem + kColS, z, id_mn);
+                else mma_ts<false>(tmem + kColU, tmem + kColS, z, id_mn);
+#pragma unroll
+                for (int ks = 1; ks < 8; ++ks)
+                    mma_ts<true>(tmem + kColU, tmem + kColS + 32 * (ks >> 1) + 8 * (ks & 1),
+                                 z + 128 * ks, id_mn);
                 if (h == 0 && now.has_m) {
-                    const uint32_t id = now.mem_t ? id_k : id_mn, by = now.mem_t ? 32 : 2048;
-#pragma unroll 1
-                    for (int ks = 0; ks < 4; ++ks)
-                        mma_bf16(tmem + kColF, sdesc_sw128(x + ks * 32, 16, 1024),
-                                 sdesc_sw128(m + ks * by, kTile, 1024), id, ks > 0 ? 1u : 0u);
+                    const uint32_t id = now.mem_t ? id_k : id_mn, by = now.mem_t ? 2 : 128;
+                    mma_ss<false>(tmem + kColF, x, m0, id);
+#pragma unroll
+                    for (int ks = 1; ks < 4; ++ks) mma_ss<true>(tmem + kColF, x + 2 * ks, m0 + by * ks, id);
                     if (now.last) mma_commit(&ctl.m_free);
                 }
                 if (h == now.nh - 1) mma_commit(&ctl.item_done[done & 1]);
