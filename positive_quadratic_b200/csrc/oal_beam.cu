@@ -589,6 +589,7 @@ int check_reorder(const void* src, int src_B, const int32_t* parents, const void
     from.B = src_B;
     if (src_B < 1) return OAL_ERR_SHAPE;
     if ((rc = check_common(&from)) || (rc = check_planes(s->B + 1ll))) return rc;
+    if (s->Hkv * state_unit_bytes() / 16 >= (size_t(1) << 31)) return OAL_ERR_SHAPE;
     if (!src || !dst || (s->B > 0 && !parents)) return OAL_ERR_NULL;
     if (!aligned16(src) || !aligned16(dst) || (reinterpret_cast<uintptr_t>(parents) & 3))
         return OAL_ERR_ALIGN;

@@ -62,7 +62,7 @@ def make(cuda, B, beams, V, dtype, seed=0):
 @pytest.mark.parametrize("B,beams,V,n", [
     (1, 1, 1, 1), (2, 1, 5, 5), (1, 2, 3, 6), (3, 4, 100, 8), (2, 4, 1000, 4), (1, 4, 1024, 32),
     (2, 3, 1025, 6), (1, 1, 2047, 32), (1, 2, 2048, 3), (2, 2, 2049, 17), (1, 8, 8191, 16),
-    (1, 4, 8193, 9), (2, 16, 16385, 32), (1, 5, 50257, 10), (40, 8, 50257, 16), (3, 1, 131072, 1)])
+    (1, 4, 8193, 9), (2, 16, 16385, 32), (1, 256, 50, 32), (1, 2, 1000003, 32), (70, 1, 33, 2), (1, 5, 50257, 10), (40, 8, 50257, 16), (3, 1, 131072, 1)])
 def test_select(cuda, dtype, B, beams, V, n):
     check_select(*make(cuda, B, beams, V, dtype), n)
 
@@ -265,3 +265,56 @@ def test_beam_search(cuda, kind):
         _decay_ref.check("state", state[:1], w[1], w[3], F32, T + steps)
     torch.cuda.synchronize()
     assert oal.device_error() == 0
+
+
+def test_select_of_many_ended_rows(cuda):
+    """256 rows, all but a few ended: their padding tokens compete by their running scores."""
+    x, run = make(cuda, 2, 256, 300, F32)
+    ended = torch.ones(2, 256, dtype=torch.uint8, device=cuda)
+    ended[0, 7] = ended[0, 250] = 0
+    check_select(x, run, 32, ended, 299)
+    check_select(torch.zeros_like(x), torch.zeros_like(run), 32, ended, 3)
+
+
+def test_select_ties_across_rows_and_tiles(cuda):
+    """Thousands of candidates that share the n-th score, in several rows and tiles."""
+    x = torch.zeros(1, 4, 40000, device=cuda)
+    x[:, :, ::7] = 2.0
+    x[0, 2, 39999] = 3.0
+    x[0, 0, 5] = 2.5
+    run = torch.tensor([[0.0, 0.0, 1.0, 1.0]], device=cuda)
+    check_select(x, run, 32)
+    check_select(x.bfloat16(), run, 20)
+    x[0, 1] = x[0, 0]  # two equal rows
+    check_select(x, run, 32)
+
+
+def test_binding_refusals(cuda):
+    x, run = make(cuda, 2, 3, 100, F32)
+    for bad in (lambda: oal.beam_select(x.half(), run, 2), lambda: oal.beam_select(x, run.double(), 2),
+                lambda: oal.beam_select(x, run, 2, ended=run)):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: oal.beam_select(x[0], run, 2), lambda: oal.beam_select(x, run[:, :2], 2),
+                lambda: oal.beam_select(x.transpose(1, 2), run, 2),
+                lambda: oal.beam_select(x[:, ::2], run[:, ::2].contiguous(), 2, tokens=run),
+                lambda: oal.beam_select(x[:, :2], run[:, :2].contiguous(), 2)):
+        with pytest.raises((ValueError, TypeError)):
+            bad()
+    for bad in (dict(n=33), dict(n=0), dict(n=2, ended=torch.ones(2, 3, dtype=torch.uint8, device=cuda),
+                                            pad_token=100)):
+        with pytest.raises(oal.OALError):
+            oal.beam_select(x, run, **bad)
+    with pytest.raises(oal.OALError):  # the rows of a misaligned view
+        oal.beam_select(x[:, :, 1:], run, 2)
+    src, *_ = quadratic_state(cuda, 2, 2, 1)
+    par = torch.zeros(2, dtype=torch.int32, device=cuda)
+    for bad in (lambda: oal.state_reorder(src, par, src[:-16], 2, 1),
+                lambda: oal.state_reorder(src[:1000], par, src, 2, 1),
+                lambda: oal.state_reorder(src, par, src.clone().cpu(), 2, 1)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(TypeError):
+        oal.state_reorder(src, par.long(), src.clone(), 2, 1)
+    with pytest.raises(oal.OALError):
+        oal.state_reorder(src, par, src, 2, 1)

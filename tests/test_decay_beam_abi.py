@@ -1,0 +1,202 @@
+"""Host-side checks of decayed linear attention, beam selection and state reordering: every refusal
+comes before the device is touched, so these run without a GPU."""
+import ctypes
+
+import pytest
+import torch
+
+from positive_quadratic_b200 import build, oal
+
+NULL, SHAPE, UNSUPPORTED, ALIGN, WORKSPACE, OVERLAP = -1, -2, -3, -4, -8, -11
+BIG = ctypes.c_size_t(1 << 60)
+SCALE = ctypes.c_float(0.125)
+
+
+@pytest.fixture(scope="module")
+def L():
+    build.build()
+    return oal.lib()
+
+
+def P(addr=1 << 20):
+    return ctypes.c_void_p(addr)
+
+
+def shape(B=2, T=100, Hq=4, Hkv=2, dtype=oal.OAL_BF16, **kw):
+    s = oal.make_shape(B, T, Hq, Hkv, 128, dtype)
+    for k, v in kw.items():
+        setattr(s, k, v)
+    return s
+
+
+def size_of(L, fn, s):
+    n = ctypes.c_size_t()
+    rc = getattr(L, fn)(ctypes.byref(s), ctypes.byref(n))
+    return rc, n.value
+
+
+def test_state_and_workspace_sizes(L):
+    assert size_of(L, "oal_decay_state_bytes", shape()) == (0, 2 * 2 * 64 * 64 * 4)
+    # fp32: the chunk states, in place; bf16: the chunk sums and the bf16 states before them
+    for T, c64, c128 in ((1, 1, 1), (64, 1, 1), (65, 2, 1), (1000, 16, 8)):
+        rc, n = size_of(L, "oal_decay_prefill_workspace_bytes", shape(T=T, dtype=oal.OAL_F32))
+        assert (rc, n) == (0, 4 * c64 * 16384)
+        rc, n = size_of(L, "oal_decay_prefill_workspace_bytes", shape(T=T))
+        assert (rc, n) == (0, 4 * c128 * (16384 + 8192))
+    assert size_of(L, "oal_decay_prefill_workspace_bytes", shape(T=0))[1] >= 256
+    # the gradient: both directions; the reverse one in parts where chunks are few (a group of 2:
+    # 2 parts), never in empty ones (a group of 7 over 64 chunks: 4 parts of 2)
+    assert size_of(L, "oal_decay_backward_workspace_bytes", shape(T=1000)) == (
+        0, 4 * 8 * (2 * 8192 + 3 * 16384))
+    assert size_of(L, "oal_decay_backward_workspace_bytes", shape(B=1, T=4096, Hq=14)) == (
+        0, 64 * (2 * 8192 + 5 * 16384))
+
+
+@pytest.mark.parametrize("field,value,code", [
+    ("Hq", 0, SHAPE), ("Hkv", 3, SHAPE), ("B", -1, SHAPE), ("T", -5, SHAPE), ("dh", 32, UNSUPPORTED),
+    ("dv", 128, UNSUPPORTED), ("dtype", 7, UNSUPPORTED), ("Hq", 18, UNSUPPORTED),
+    ("T", 1 << 30, SHAPE)])
+def test_shapes_are_checked(L, field, value, code):
+    s = shape(**{field: value})
+    for fn in ("oal_decay_prefill_workspace_bytes", "oal_decay_backward_workspace_bytes"):
+        assert size_of(L, fn, s)[0] == code
+    assert L.oal_decay_prefill(P(), P(), P(), P(), SCALE, None, P(), P(), P(), BIG, ctypes.byref(s),
+                               None) == code
+    if field != "T":
+        assert L.oal_decay_step(P(), P(), P(), P(), SCALE, None, 0, None, P(), P(), ctypes.byref(s),
+                                None) == code
+
+
+def test_grid_limits(L):
+    s = shape(B=32768, T=1)  # B * Hq = 131072 blocks in y
+    assert size_of(L, "oal_decay_prefill_workspace_bytes", s)[0] == SHAPE
+    assert size_of(L, "oal_decay_state_bytes", s)[0] == 0  # a step has no such limit
+
+
+def call_prefill(L, s, fn="oal_decay_prefill", q=P(), k=P(), v=P(), g=P(), lens=None, out=P(),
+                 state=P(), ws=P(), n=BIG):
+    return getattr(L, fn)(q, k, v, g, SCALE, lens, out, state, ws, n, ctypes.byref(s), None)
+
+
+@pytest.mark.parametrize("dtype", [oal.OAL_F32, oal.OAL_BF16])
+def test_prefill_arguments(L, dtype):
+    s = shape(dtype=dtype)
+    for fn in ("oal_decay_prefill", "oal_decay_prefill_continue"):
+        for name in ("q", "k", "v", "g"):
+            assert call_prefill(L, s, fn, **{name: None}) == NULL, name
+        for name in ("q", "k", "v", "out", "state", "ws"):
+            assert call_prefill(L, s, fn, **{name: P((1 << 20) + 8)}) == ALIGN, name
+        for name in ("g", "lens"):
+            assert call_prefill(L, s, fn, **{name: P((1 << 20) + 2)}) == ALIGN, name
+        assert call_prefill(L, s, fn, ws=None) == WORKSPACE
+        assert call_prefill(L, s, fn, n=ctypes.c_size_t(64)) == WORKSPACE
+    assert call_prefill(L, s, out=None, state=None) == NULL
+    assert call_prefill(L, s, "oal_decay_prefill_continue", state=None) == NULL
+    assert L.oal_decay_prefill(P(), P(), P(), P(), SCALE, None, P(), P(), P(), BIG, None, None) == NULL
+    # nothing to do: no sequence; no token to continue with
+    assert call_prefill(L, shape(B=0, dtype=dtype), q=None, k=None, v=None, out=None, state=None) == 0
+    assert call_prefill(L, shape(T=0, dtype=dtype), "oal_decay_prefill_continue", q=None, k=None,
+                        v=None, out=None) == 0
+
+
+def test_backward_arguments(L):
+    s = shape()
+    names = ("q", "k", "v", "g", "lens", "dout", "state", "dlast", "dq", "dk", "dv", "dstate")
+
+    def call(ws=P(), n=BIG, **kw):
+        a = dict.fromkeys(names, P())
+        a.update(lens=None, state=None, dlast=None, dstate=None)
+        a.update(kw)
+        return L.oal_decay_backward(a["q"], a["k"], a["v"], a["g"], SCALE, a["lens"], a["dout"],
+                                    a["state"], a["dlast"], a["dq"], a["dk"], a["dv"], a["dstate"], ws,
+                                    n, ctypes.byref(s), None)
+
+    for name in ("q", "k", "v", "g", "dout", "dq", "dk", "dv"):
+        assert call(**{name: None}) == NULL, name
+    for name in names:
+        off = 2 if name in ("g", "lens") else 8
+        assert call(**{name: P((1 << 20) + off)}) == ALIGN, name
+    assert call(ws=None) == WORKSPACE and call(n=ctypes.c_size_t(1 << 10)) == WORKSPACE
+
+
+def test_step_arguments(L):
+    s = shape(T=1)
+    size = 2 * 2 * 16384
+
+    def call(q=P(), k=P(), v=P(), g=P(), src=None, n=0, parents=None, state=P(), out=P()):
+        return L.oal_decay_step(q, k, v, g, SCALE, src, n, parents, state, out, ctypes.byref(s), None)
+
+    for name in ("q", "k", "v", "g", "state", "out"):
+        assert call(**{name: None}) == NULL, name
+    for name in ("q", "k", "v", "state", "out"):
+        assert call(**{name: P((1 << 20) + 8)}) == ALIGN, name
+    far = P((1 << 20) + size)
+    assert call(src=far, n=2) == NULL and call(parents=P(), n=2) == NULL  # they go together
+    assert call(src=far, n=0, parents=P()) == SHAPE
+    assert call(src=P((1 << 20) + size - 16), n=2, parents=P()) == OVERLAP
+    assert call(src=P((1 << 20) - size + 16), n=2, parents=P()) == OVERLAP
+    assert call(src=P(1 << 20), n=2, parents=P()) == OVERLAP
+
+
+def select(L, logits=P(), ld=1000, dtype=oal.OAL_BF16, running=P(), ended=None, pad=0, B=2, beams=4,
+           V=1000, n=4, scores=P(), parents=P(), tokens=P(), ws=P(), nb=BIG):
+    return L.oal_beam_select(logits, ld, dtype, running, ended, pad, B, beams, V, n, scores, parents,
+                             tokens, ws, nb, None)
+
+
+def test_select_arguments(L):
+    for kw in (dict(B=-1), dict(beams=0), dict(V=0), dict(n=0), dict(ld=999), dict(beams=1, V=3, n=4, ld=3),
+               dict(B=20000), dict(V=(1 << 29) - 1, ld=1 << 30),
+               dict(ended=P(), pad=1000), dict(ended=P(), pad=-1)):
+        assert select(L, **kw) == SHAPE, kw
+    for kw in (dict(n=33), dict(beams=257), dict(dtype=2)):
+        assert select(L, **kw) == UNSUPPORTED, kw
+    for name in ("logits", "running", "scores", "parents", "tokens"):
+        assert select(L, **{name: None}) == NULL, name
+        assert select(L, **{name: P((1 << 20) + 2)}) == ALIGN, name
+    assert select(L, ws=None) == WORKSPACE and select(L, nb=ctypes.c_size_t(1)) == WORKSPACE
+    assert select(L, B=0, logits=None, running=None) == 0
+    n = ctypes.c_size_t()
+    assert L.oal_beam_select_workspace_bytes(2, 4, 1000, 33, 0, ctypes.byref(n)) == UNSUPPORTED
+    assert L.oal_beam_select_workspace_bytes(2, 4, 1000, 4, 0, None) == NULL
+
+
+def test_reorder_arguments(L):
+    s = shape(B=3)
+    size = oal.state_bytes(s)
+    a, b = 1 << 30, (1 << 30) + size
+    r = lambda src=P(a), n=3, par=P(), dst=P(b), s=s: L.oal_state_reorder(  # noqa: E731
+        src, n, par, dst, ctypes.byref(s), None)
+    assert r(src=None) == NULL and r(par=None) == NULL and r(dst=None) == NULL
+    assert r(n=0) == SHAPE and r(s=shape(B=70000, T=1)) == SHAPE
+    assert r(src=P(a + 8)) == ALIGN and r(dst=P(b + 8)) == ALIGN and r(par=P(a + 2)) == ALIGN
+    assert r(dst=P(a)) == OVERLAP and r(dst=P(b - 16)) == OVERLAP
+    d = lambda src, dst, n=3: L.oal_decay_state_reorder(  # noqa: E731
+        src, n, P(), dst, ctypes.byref(s), None)
+    rows = 3 * 2 * 16384
+    assert d(P(a), P(a + rows - 16)) == OVERLAP and d(None, P(a)) == NULL
+    z = shape(B=0)
+    assert L.oal_decay_state_reorder(P(a), 3, None, P(b), ctypes.byref(z), None) == 0
+    beam = lambda q=P(), src=P(a), n=3, par=P(), dst=P(b), out=P(), ws=P(), nb=BIG: (  # noqa: E731
+        L.oal_decode_step_beam(q, P(), P(), src, n, par, dst, out, ws, nb, ctypes.byref(s), None))
+    assert beam(q=None) == NULL and beam(par=None) == NULL and beam(out=P(8)) == ALIGN
+    assert beam(ws=None) == WORKSPACE and beam(nb=ctypes.c_size_t(16)) == WORKSPACE
+    assert beam(dst=P(a + 16)) == OVERLAP and beam(n=0) == SHAPE
+
+
+def test_binding_refuses_host_tensors():
+    q, k = torch.zeros(1, 2, 1, 64), torch.zeros(1, 1, 1, 64)
+    g, state = torch.zeros(1), torch.zeros(1, 1, 64, 64)
+    i32 = torch.zeros(1, dtype=torch.int32)
+    buf = torch.zeros(oal.state_bytes(oal.make_shape(1, 1, 2, 1)), dtype=torch.uint8)
+    for call in (lambda: oal.decay_prefill(q, k, k, g, 0.1),
+                 lambda: oal.decay_prefill_continue(q, k, k, g, 0.1, state),
+                 lambda: oal.decay_step(q, k, k, g, 0.1, state),
+                 lambda: oal.decay_step(q=q, k=k, v=k, log_decay=g, scale=0.1, state=state),
+                 lambda: oal.decay_backward(q, k, k, g, 0.1, q),
+                 lambda: oal.beam_select(torch.zeros(1, 1, 5), torch.zeros(1, 1), 2),
+                 lambda: oal.state_reorder(buf, i32, buf.clone(), 2, 1),
+                 lambda: oal.decay_state_reorder(state, i32, state.clone()),
+                 lambda: oal.decode_step_beam(q, k, k, buf, i32, buf.clone(), buf)):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()

@@ -1,6 +1,9 @@
 """Linear attention with a decay per head on the GPU: prompts, continuation, single tokens and
 gradients against a plain 64-bit implementation, and the calls around them."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -312,3 +315,88 @@ def test_long_prompt(cuda, dtype):
     w = torch.exp(-1e-3 * torch.arange(T - 1, -1, -1).double())[:, None]
     ref.check("state", state[0, 0], (w * kd[0, 0]).T @ vd[0, 0],
               (w * kd[0, 0].abs()).T @ vd[0, 0].abs(), F32, T)
+
+
+def test_first_call_inside_a_capture(cuda):
+    """A process whose first call is captured: nothing of the call's set-up breaks the capture."""
+    code = """
+import torch
+from positive_quadratic_b200 import oal
+torch.manual_seed(0)
+q, k, v = (torch.randn(1, h, 300, 64, device="cuda").bfloat16() for h in (2, 1, 1))
+g, ws = torch.full((1,), -0.1, device="cuda"), torch.empty(1 << 22, dtype=torch.uint8, device="cuda")
+x, run = torch.randn(1, 2, 5000, device="cuda"), torch.zeros(1, 2, device="cuda")
+torch.cuda.synchronize()
+G = torch.cuda.CUDAGraph()
+with torch.cuda.graph(G):
+    out, state = oal.decay_prefill(q, k, v, g, 0.125, workspace=ws)
+    best = oal.beam_select(x, run, 4, workspace=ws[1 << 21:])
+    dq = oal.decay_backward(q, k, v, g, 0.125, out, workspace=ws)["dq"]
+G.replay()
+o, s = oal.decay_prefill(q, k, v, g, 0.125)
+assert torch.equal(out, o) and torch.equal(state, s)
+assert torch.equal(dq, oal.decay_backward(q, k, v, g, 0.125, out)["dq"])
+assert all(torch.equal(a, b) for a, b in zip(best, oal.beam_select(x, run, 4)))
+assert oal.device_error() == 0
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([sys.executable, "-c", code], cwd=root, check=True, timeout=300)
+
+
+def test_two_streams_at_once(cuda):
+    """Calls on two streams with workspaces of their own do not disturb one another."""
+    a = make(cuda, 2, 700, 14, 2, BF, seed=1)
+    b = make(cuda, 1, 900, 4, 4, BF, seed=2)
+    want = [oal.decay_prefill(*x[:3], x[3], SCALE) for x in (a, b)]
+    grads = [oal.decay_backward(*x[:3], x[3], SCALE, x[4]) for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got, got_g = [], []
+    for _ in range(5):
+        for x, s in zip((a, b), streams):
+            got.append(oal.decay_prefill(*x[:3], x[3], SCALE, stream=s))
+            got_g.append(oal.decay_backward(*x[:3], x[3], SCALE, x[4], stream=s))
+    torch.cuda.synchronize()
+    for i, (x, y) in enumerate(zip(got, got_g)):
+        assert all(torch.equal(p, q) for p, q in zip(x, want[i % 2]))
+        assert all(torch.equal(y[n], grads[i % 2][n]) for n in y)
+    clean()
+
+
+def test_binding_refusals(cuda):
+    q, k, v, g, do, S, R = make(cuda, 2, 10, 4, 2, BF, state=True)
+    ok = lambda **kw: oal.decay_prefill(**{**dict(  # noqa: E731
+        q=q, k=k, v=v, log_decay=g, scale=SCALE), **kw})
+    ok()
+    for bad in (dict(k=k.float()), dict(log_decay=g.double()), dict(q=q.half()),
+                dict(lens=torch.zeros(2, dtype=torch.int64, device=cuda)), dict(out=q.float()),
+                dict(state=S.bfloat16())):
+        with pytest.raises(TypeError):
+            ok(**bad)
+    for bad in (dict(k=k[:, :, :9].contiguous()), dict(v=v[:1].contiguous()), dict(log_decay=g[:1]),
+                dict(q=q.transpose(1, 2)), dict(k=k.cpu()), dict(out=q[:, :2]), dict(state=S[:1]),
+                dict(lens=torch.zeros(3, dtype=torch.int32, device=cuda)),
+                dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            ok(**bad)
+    with pytest.raises(oal.OALError):  # heads that do not divide, another head dimension
+        oal.decay_prefill(q[:, :3].contiguous(), k, v, g, SCALE)
+    with pytest.raises(oal.OALError):
+        oal.decay_prefill(*[x[..., :32].contiguous() for x in (q, k, v)], g, SCALE)
+    with pytest.raises(oal.OALError):
+        ok(workspace=torch.empty(256, dtype=torch.uint8, device=cuda))
+    with pytest.raises(ValueError):
+        oal.decay_prefill_continue(q, k, v, g, SCALE, None)
+    one = [x[:, :, :1].contiguous() for x in (q, k, v)]
+    par = torch.zeros(2, dtype=torch.int32, device=cuda)
+    for args in (dict(src=S), dict(parents=par), dict(src=S, parents=par[:1]),
+                 dict(src=S[..., :32].contiguous(), parents=par)):
+        with pytest.raises(ValueError):
+            oal.decay_step(*one, g, SCALE, R, **args)
+    with pytest.raises(oal.OALError):  # in place through parents
+        oal.decay_step(*one, g, SCALE, S, src=S, parents=par)
+    with pytest.raises(ValueError):
+        oal.decay_step(q, k, v, g, SCALE, S)
+    with pytest.raises(TypeError):
+        oal.decay_backward(q, k, v, g, SCALE, do.float())
+    clean()
