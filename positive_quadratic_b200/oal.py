@@ -827,9 +827,10 @@ def _parents(parents, B, index):
     return _need("parents", parents, parents.shape, torch.int32, index)
 
 
-def beam_select_workspace(B, beams, V, n, device, dtype=torch.float32) -> torch.Tensor:
-    """A workspace for beam_select of these sizes (either type of logits)."""
-    return empty_workspace(_select_bytes(B, beams, V, n, OAL_F32), device)
+def beam_select_workspace(B, beams, V, n, device) -> torch.Tensor:
+    """A workspace for beam_select of these sizes, for either type of logits."""
+    need = max(_select_bytes(B, beams, V, n, code) for code in (OAL_F32, OAL_BF16))
+    return empty_workspace(need, device)
 
 
 def _select_bytes(B, beams, V, n, code) -> int:

@@ -68,6 +68,17 @@ def test_select(cuda, dtype, B, beams, V, n):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("V", [8185, 8187, 8189, 16381])
+def test_select_in_a_made_workspace(cuda, dtype, V):
+    """One workspace serves logits of either type, at lengths where theirs differ too."""
+    x, run = make(cuda, 2, 3, V, dtype)
+    ws = oal.beam_select_workspace(2, 3, V, 5, cuda)
+    got = oal.beam_select(x, run, 5, workspace=ws)
+    _, parents, tokens = plain_select(x, run, 5)
+    assert (got[1].cpu().numpy() == parents).all() and (got[2].cpu().numpy() == tokens).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("V", [7, 1500, 9001, 70000])
 def test_select_ties(cuda, dtype, V):
     """Equal logits (all of them, and a few values over and over) in the order of their places;

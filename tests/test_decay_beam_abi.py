@@ -161,6 +161,15 @@ def test_select_arguments(L):
     assert L.oal_beam_select_workspace_bytes(2, 4, 1000, 4, 0, None) == NULL
 
 
+@pytest.mark.parametrize("V", [1, 7, 8185, 8186, 8187, 8189, 8190, 8192, 8195, 16381])
+def test_select_workspace_holds_either_type(V):
+    """A bf16 row may begin up to 7 logits behind a 16-byte boundary, an fp32 row 3: one tile more
+    for some lengths."""
+    ws = oal.beam_select_workspace(2, 3, V, 1, "cpu")
+    assert all(ws.numel() >= oal._select_bytes(2, 3, V, 1, code)
+               for code in (oal.OAL_BF16, oal.OAL_F32))
+
+
 def test_reorder_arguments(L):
     s = shape(B=3)
     size = oal.state_bytes(s)
