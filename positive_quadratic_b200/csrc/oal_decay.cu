@@ -456,7 +456,7 @@ constexpr int kSms = 148;
 int parts_of(const oal_shape* s, int grp)
 {
     const long long items = (long long)s->B * s->Hkv * chunks_of(s);
-    if (!on_tensor_cores(s) || chunks_of(s) <= 1) return 1;
+    if (!on_tensor_cores(s) || chunks_of(s) <= 1 || s->B == 0) return 1;
     const int parts = int(std::min<long long>(grp, (2 * kSms + items - 1) / items));
     const int per = (grp + parts - 1) / parts;
     return (grp + per - 1) / per;  // none of them empty

@@ -52,6 +52,13 @@ def test_state_and_workspace_sizes(L):
         0, 64 * (2 * 8192 + 5 * 16384))
 
 
+@pytest.mark.parametrize("dtype", [oal.OAL_F32, oal.OAL_BF16])
+@pytest.mark.parametrize("T", [0, 1, 300])
+def test_sizes_of_an_empty_batch(L, T, dtype):
+    for fn in ("oal_decay_prefill_workspace_bytes", "oal_decay_backward_workspace_bytes"):
+        assert size_of(L, fn, shape(B=0, T=T, dtype=dtype)) == (0, 256)
+
+
 @pytest.mark.parametrize("field,value,code", [
     ("Hq", 0, SHAPE), ("Hkv", 3, SHAPE), ("B", -1, SHAPE), ("T", -5, SHAPE), ("dh", 32, UNSUPPORTED),
     ("dv", 128, UNSUPPORTED), ("dtype", 7, UNSUPPORTED), ("Hq", 18, UNSUPPORTED),
