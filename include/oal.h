@@ -468,7 +468,7 @@ int oal_beam_select_workspace_bytes(int B, int beams, int V, int n, int dtype, s
  * be (a logit of -inf; a row with a NaN or +inf logit, with no finite logit, or whose running
  * score is not finite; another token of an ended row) scores -inf, and is returned where no
  * others are left.  Scores are formed in 64 bits and rounded once.
- * n <= 32, n <= beams * V, beams <= 256, beams * V < 2^31 - 64, B * beams <= 65535. */
+ * n <= 32, n <= beams * V, beams <= 256, beams * V < 2^31 - 2^14, B * beams <= 65535. */
 int oal_beam_select(const void* logits, long long row_stride, int dtype, const float* running,
                     const uint8_t* ended, int pad_token, int B, int beams, int V, int n,
                     float* scores, int32_t* parents, int32_t* tokens, void* workspace,

@@ -541,12 +541,13 @@ SelectLayout select_layout(int dtype, int rows, int V)
     return l;
 }
 
+// (A tile may reach past the last logit, by less than two tiles: its places stay below 2^31.)
 int check_select(int B, int beams, int V, int n, int dtype)
 {
     if (B < 0 || beams < 1 || V < 1 || n < 1) return OAL_ERR_SHAPE;
     if (dtype != OAL_F32 && dtype != OAL_BF16) return OAL_ERR_UNSUPPORTED;
     if (n > kMaxSelect || beams > kMaxBeams) return OAL_ERR_UNSUPPORTED;
-    if ((long long)n > (long long)beams * V || (long long)beams * V >= (1LL << 31) - 64 ||
+    if ((long long)n > (long long)beams * V || (long long)beams * V >= (1LL << 31) - 2 * kTile ||
         (long long)B * beams > kMaxGridPlanes)
         return OAL_ERR_SHAPE;
     return OAL_OK;

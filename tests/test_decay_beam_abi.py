@@ -168,6 +168,18 @@ def test_select_arguments(L):
     assert L.oal_beam_select_workspace_bytes(2, 4, 1000, 4, 0, None) == NULL
 
 
+def test_largest_vocabularies(L):
+    """Places of the last tile count up to two tiles past V, in 32 bits."""
+    n = ctypes.c_size_t()
+    size = lambda beams, V, dt: L.oal_beam_select_workspace_bytes(  # noqa: E731
+        1, beams, V, 1, dt, ctypes.byref(n))
+    for dt in (oal.OAL_F32, oal.OAL_BF16):
+        assert size(1, (1 << 31) - (1 << 14) - 1, dt) == 0
+        assert size(1, (1 << 31) - (1 << 14), dt) == SHAPE
+        assert size(1, (1 << 31) - 65, dt) == SHAPE
+        assert size(8, (1 << 28) - (1 << 11), dt) == SHAPE
+
+
 @pytest.mark.parametrize("V", [1, 7, 8185, 8186, 8187, 8189, 8190, 8192, 8195, 16381])
 def test_select_workspace_holds_either_type(V):
     """A bf16 row may begin up to 7 logits behind a 16-byte boundary, an fp32 row 3: one tile more
