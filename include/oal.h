@@ -401,6 +401,8 @@ int oal_state_prefix_sum(const float* parts, int n_parts, size_t n, float* out, 
  *    0 <= lens[b] <= T.  What lies behind them in q, k, v (and dout) is not used, whatever it
  *    holds, and the rows behind them of out (and of the gradients) are left as they were.  An
  *    entry out of range sets OAL_ERR_VALUE and is clamped;
+ *  - outputs, gradients and states that are written must not overlap the inputs or one another
+ *    (OAL_ERR_OVERLAP);
  *  - oal_shape.chunk is not used.
  * Within a sequence, a token that holds an infinity or a NaN may reach every row of its chunk of
  * 128 tokens, earlier rows included, and every later row.  bf16 inputs are multiplied on tensor
@@ -446,7 +448,7 @@ int oal_decay_backward_workspace_bytes(const oal_shape* s, size_t* bytes);
  * the last token) [B][Hkv][64][64] fp32 or NULL for zero:
  *     dq [B][Hq][T][64], dk and dv [B][Hkv][T][64] (summed over the query heads of a key/value
  *     head), dstate [B][Hkv][64][64] fp32 = dLoss/d(state before the first token), or NULL.
- * dstate may be dlast.  The states are recomputed; nothing of the forward pass has to be kept. */
+ * dstate may be dlast itself.  The states are recomputed; nothing of the forward pass has to be kept. */
 int oal_decay_backward(const void* q, const void* k, const void* v, const float* log_decay,
                        float scale, const int32_t* lens, const void* dout, const float* state,
                        const float* dlast, void* dq, void* dk, void* dv, float* dstate,
@@ -463,6 +465,7 @@ int oal_beam_select_workspace_bytes(int B, int beams, int V, int n, int dtype, s
  *   first 16-byte aligned; running [B * beams] fp32; ended [B * beams] bytes, or NULL;
  *   scores [B][n] fp32, parents [B][n] int32 (rows of the B * beams, as oal_state_reorder and the
  *   beam steps take them), tokens [B][n] int32, best first.
+ * The results must not overlap one another, running or ended (OAL_ERR_OVERLAP).
  * Equal scores come in the order of (row, token).  An ended row (ended[r] != 0) goes on with
  * pad_token alone, at its running score, and its logits are not read.  A candidate that cannot
  * be (a logit of -inf; a row with a NaN or +inf logit, with no finite logit, or whose running

@@ -20,6 +20,26 @@ bool overlap(const void* a, size_t na, const void* b, size_t nb)
     return x < y + nb && y < x + na;
 }
 
+// An array that a call reads or writes.
+struct Span {
+    const void* p;
+    size_t bytes;
+};
+// Whether one that the call writes shares bytes with another one of its arrays (NULL: none).
+template <size_t kW, size_t kR>
+bool any_overlap(const Span (&written)[kW], const Span (&read)[kR])
+{
+    for (size_t i = 0; i < kW; ++i) {
+        const Span& w = written[i];
+        if (!w.p || !w.bytes) continue;
+        for (const Span& r : read)
+            if (r.p && r.bytes && overlap(w.p, w.bytes, r.p, r.bytes)) return true;
+        for (size_t j = 0; j < i; ++j)
+            if (written[j].p && overlap(w.p, w.bytes, written[j].p, written[j].bytes)) return true;
+    }
+    return false;
+}
+
 // q, k, v, out: required and aligned only when there is at least one token to process.
 int check_io(const oal_shape* s, const void* q, const void* k, const void* v, const void* out)
 {

@@ -633,6 +633,10 @@ int oal_beam_select(const void* logits, long long row_stride, int dtype, const f
     if ((rc = oal_beam_select_workspace_bytes(B, beams, V, n, dtype, &need))) return rc;
     if (!workspace || workspace_bytes < need) return OAL_ERR_WORKSPACE;
     if (!aligned16(workspace)) return OAL_ERR_ALIGN;
+    const size_t n_out = size_t(B) * n * 4;
+    if (any_overlap({{scores, n_out}, {parents, n_out}, {tokens, n_out}},
+                    {{running, size_t(B) * beams * 4}, {ended, size_t(B) * beams}}))
+        return OAL_ERR_OVERLAP;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const auto go = dtype == OAL_BF16 ? beam::launch_select<__nv_bfloat16>
                                       : beam::launch_select<float>;

@@ -611,6 +611,12 @@ int check(const oal_shape* s)
     return check_planes((long long)s->B * s->Hq);
 }
 
+// Bytes of T tokens of `heads` heads.
+size_t io_bytes(const oal_shape* s, int heads)
+{
+    return size_t(s->B) * heads * s->T * kD * (s->dtype == OAL_BF16 ? 2 : 4);
+}
+
 size_t state_bytes(const oal_shape* s) { return size_t(s->B) * s->Hkv * kDecayState * 4; }
 
 int prefill(const void* q, const void* k, const void* v, const float* log_decay, float scale,
@@ -629,6 +635,9 @@ int prefill(const void* q, const void* k, const void* v, const float* log_decay,
     if ((rc = oal_decay_prefill_workspace_bytes(s, &need))) return rc;
     if (!ws || ws_bytes < need) return OAL_ERR_WORKSPACE;
     if (!aligned16(ws)) return OAL_ERR_ALIGN;
+    const size_t nq = io_bytes(s, s->Hq), nk = io_bytes(s, s->Hkv);
+    if (any_overlap({{out, nq}, {state, state_bytes(s)}}, {{out ? q : nullptr, nq}, {k, nk}, {v, nk}}))
+        return OAL_ERR_OVERLAP;
     if (cont && s->T == 0) return OAL_OK;
     OAL_CUDA_TRY(set_attributes_once());
     const DecayShape S{s->B, s->T, s->Hkv, chunks_of(s), lens, log_decay, scale};
@@ -707,6 +716,9 @@ int oal_decay_step(const void* q, const void* k, const void* v, const float* log
         if (overlap(src, decay::state_bytes(&from), state, decay::state_bytes(s)))
             return OAL_ERR_OVERLAP;
     }
+    const size_t nq = decay::io_bytes(&one, s->Hq), nk = decay::io_bytes(&one, s->Hkv);
+    if (any_overlap({{out, nq}, {state, decay::state_bytes(s)}}, {{q, nq}, {k, nk}, {v, nk}}))
+        return OAL_ERR_OVERLAP;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return decay::by_type(s->dtype, [&](auto t) {
         using T = decltype(t);
@@ -748,6 +760,12 @@ int oal_decay_backward(const void* q, const void* k, const void* v, const float*
     if ((rc = oal_decay_backward_workspace_bytes(s, &need))) return rc;
     if (!workspace || workspace_bytes < need) return OAL_ERR_WORKSPACE;
     if (!aligned16(workspace)) return OAL_ERR_ALIGN;
+    const size_t nq = decay::io_bytes(s, s->Hq), nk = decay::io_bytes(s, s->Hkv);
+    const size_t ns = decay::state_bytes(s);
+    if (any_overlap({{dq, nq}, {dk, nk}, {dv, nk}, {dstate, ns}},
+                    {{q, nq}, {k, nk}, {v, nk}, {dout, nq}, {state, ns}}) ||
+        (dstate != dlast && dstate && dlast && overlap(dstate, ns, dlast, ns)))
+        return OAL_ERR_OVERLAP;
     OAL_CUDA_TRY(decay::set_attributes_once());
     const DecayShape S{s->B, s->T, s->Hkv, decay::chunks_of(s), lens, log_decay, scale};
     cudaStream_t st = static_cast<cudaStream_t>(stream);

@@ -189,6 +189,63 @@ def test_select_workspace_holds_either_type(V):
                for code in (oal.OAL_BF16, oal.OAL_F32))
 
 
+A, STEP = 1 << 32, 1 << 24  # places far apart
+
+
+def apart(*names):
+    return {name: A + i * STEP for i, name in enumerate(names)}
+
+
+def ptrs(d):
+    return {k: P(v) for k, v in d.items()}
+
+
+@pytest.mark.parametrize("dtype", [oal.OAL_F32, oal.OAL_BF16])
+@pytest.mark.parametrize("fn", ["oal_decay_prefill", "oal_decay_prefill_continue"])
+def test_prefill_over_its_inputs(L, fn, dtype):
+    s = shape(dtype=dtype)
+    at = apart("q", "k", "v", "g", "out", "state", "ws")
+    for w in ("out", "state"):
+        for r in ("q", "k", "v", "out"):
+            if w != r:
+                assert call_prefill(L, s, fn, **ptrs({**at, w: at[r]})) == OVERLAP, (w, r)
+                assert call_prefill(L, s, fn, **ptrs({**at, w: at[r] + 16})) == OVERLAP, (w, r)
+
+
+def test_step_over_its_inputs(L):
+    s = shape(T=77)  # T is not used: one token
+    at = apart("q", "k", "v", "g", "state", "out")
+    for w in ("out", "state"):
+        for r in ("q", "k", "v", "out"):
+            if w != r:
+                a = ptrs({**at, w: at[r]})
+                assert L.oal_decay_step(a["q"], a["k"], a["v"], a["g"], SCALE, None, 0, None, a["state"],
+                                        a["out"], ctypes.byref(s), None) == OVERLAP, (w, r)
+
+
+def test_backward_over_its_inputs(L):
+    s = shape()
+    ins, outs = ("q", "k", "v", "dout", "state"), ("dq", "dk", "dv", "dstate")
+    at = apart(*ins, *outs, "g", "dlast", "ws")
+    for w in outs:
+        for r in ins + outs + ("dlast",):
+            off = 16 if r == "dlast" else 0  # dlast itself may be dstate
+            if w == r or (r == "dlast" and w != "dstate"):
+                continue
+            a = ptrs({**at, w: at[r] + off})
+            assert L.oal_decay_backward(
+                a["q"], a["k"], a["v"], a["g"], SCALE, None, a["dout"], a["state"], a["dlast"], a["dq"],
+                a["dk"], a["dv"], a["dstate"], a["ws"], BIG, ctypes.byref(s), None) == OVERLAP, (w, r)
+
+
+def test_select_over_its_inputs(L):
+    at = apart("logits", "running", "ended", "scores", "parents", "tokens", "ws")
+    for w in ("scores", "parents", "tokens"):
+        for r in ("running", "ended", "scores", "parents", "tokens"):
+            if w != r:
+                assert select(L, **ptrs({**at, w: at[r]})) == OVERLAP, (w, r)
+
+
 def test_reorder_arguments(L):
     s = shape(B=3)
     size = oal.state_bytes(s)
