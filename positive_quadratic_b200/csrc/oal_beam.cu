@@ -686,6 +686,7 @@ int oal_decode_step_beam(const void* q, const void* k, const void* v, const void
     if (overlap(src, state_bytes(src_B, s->Hq, s->Hkv), dst,
                       state_bytes(s->B, s->Hq, s->Hkv)))
         return OAL_ERR_OVERLAP;
+    if (s->B == 0) return oal_state_reorder(src, src_B, parents, dst, s, stream);  // tables alone
     return launch_decode(q, k, v, dst, out,
                          reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) +
                                                   decode_ticket_bytes(s)),

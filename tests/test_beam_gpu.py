@@ -197,6 +197,19 @@ def test_decode_step_beam(cuda, dtype, B, n, Hq, Hkv):
     assert oal.device_error() == 0
 
 
+def test_decode_step_beam_of_no_sequence(cuda):
+    """dst becomes the empty state that the reordering and the step leave."""
+    src, *_ = quadratic_state(cuda, 2, 4, 2)
+    par = torch.empty(0, dtype=torch.int32, device=cuda)
+    q, k = (torch.empty(0, h, 1, 64, dtype=BF, device=cuda) for h in (4, 2))
+    size = oal.state_bytes(oal.make_shape(0, 1, 4, 2))
+    one, two = (torch.full((size,), 0xAB, dtype=torch.uint8, device=cuda) for _ in range(2))
+    ws = oal.decode_workspace(1, 4, 2, cuda)
+    oal.decode_step_beam(q, k, k, src, par, one, ws)
+    oal.state_reorder(src, par, two, 4, 2)
+    assert torch.equal(one, two) and (one != 0xAB).any()
+
+
 def test_bad_parents_reach_the_error_word(cuda):
     src, *_ = quadratic_state(cuda, 2, 2, 1)
     par = torch.tensor([7, -1], dtype=torch.int32, device=cuda)
