@@ -51,7 +51,9 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
 {
     extern __shared__ __align__(16) unsigned char smem_raw[];
     DeltaSmem& sm = *reinterpret_cast<DeltaSmem*>(smem_raw);
+    // the first sum, then the parts of the second (the first has one)
     const DecaySum& J = blockIdx.z ? b2 : a;
+    const int part = blockIdx.z ? blockIdx.z - 1 : 0;
     const int c = blockIdx.x, bkv = blockIdx.y, b = bkv / S.Hkv, kv = bkv % S.Hkv;
     tc::grid_dep_launch();
     const int n = min(kC, decay_len(S, b) - c * kC);
@@ -63,8 +65,9 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
                                 make_float4(0.f, 0.f, 0.f, 0.f));
         return;
     }
-    const int grp = J.hy / S.Hkv;
-    const size_t plane = (size_t(b) * J.hy + kv * grp) * S.T * kD, next = size_t(S.T) * kD;
+    const int grp = J.hy / S.Hkv, per = (grp + J.parts - 1) / J.parts;
+    const int h0 = part * per, nh = min(per, grp - h0);
+    const size_t plane = (size_t(b) * J.hy + kv * grp + h0) * S.T * kD, next = size_t(S.T) * kD;
     auto fetch = [&](int h) {
         fetch_tile(sm.Y[h & 1], static_cast<const float*>(J.y) + plane + h * next, c * kC, n);
         fetch_tile(sm.Z[h & 1], static_cast<const float*>(J.z) + plane + h * next, c * kC, n);
@@ -76,8 +79,8 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
         sm.w[threadIdx.x] = J.rev ? S.scale * decay_pow(g, threadIdx.x + 1)
                                   : decay_pow(g, max(0, n - 1 - int(threadIdx.x)));
     float2 acc[4][2] = {};
-    for (int h = 0; h < grp; ++h) {
-        if (h + 1 < grp) {
+    for (int h = 0; h < nh; ++h) {
+        if (h + 1 < nh) {
             fetch(h + 1);
             fetch_wait<1>();
         } else {
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
         }
         __syncthreads();
     }
-    float* out = J.delta + (size_t(bkv) * S.chunks + c) * kDecayState;
+    float* out = J.delta + ((size_t(part) * S.B * S.Hkv + bkv) * S.chunks + c) * kDecayState;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int e = (4 * ty + i) * kDV + 4 * tx;
@@ -456,7 +459,7 @@ constexpr int kSms = 148;
 int parts_of(const oal_shape* s, int grp)
 {
     const long long items = (long long)s->B * s->Hkv * chunks_of(s);
-    if (!on_tensor_cores(s) || chunks_of(s) <= 1 || s->B == 0) return 1;
+    if (chunks_of(s) <= 1 || s->B == 0) return 1;
     const int parts = int(std::min<long long>(grp, (2 * kSms + items - 1) / items));
     const int per = (grp + parts - 1) / parts;
     return (grp + per - 1) / per;  // none of them empty
@@ -556,8 +559,8 @@ int launch_sums(const DecayShape& S, const DecaySum* a, int n, const oal_shape* 
             }
             dtc::delta_kernel<<<items, dtc::kThreads, dtc::kDeltaSmem, st>>>(maps, S, a[0], b2);
         } else {
-            delta_simt_kernel<<<dim3(S.chunks, planes, n), kThreads, sizeof(DeltaSmem), st>>>(S, a[0],
-                                                                                             b2);
+            delta_simt_kernel<<<dim3(S.chunks, planes, n == 1 ? 1 : 1 + b2.parts), kThreads,
+                                sizeof(DeltaSmem), st>>>(S, a[0], b2);
         }
         OAL_LAUNCH_CHECK();
     }
