@@ -259,13 +259,13 @@ __device__ __forceinline__ void row_products(const float (*A)[kLd], const float 
         for (int e = 0; e < 4; ++e) s[i][e] = acc[i][e].x + acc[i][e].y;
 }
 
-// acc[i] += row 4 ty + i of A times B, columns 4 tx .. + 3
+// acc[i] += row 4 ty + i of A times B, columns 4 tx .. + 3, over k0 <= k < k1 (multiples of 4)
 __device__ __forceinline__ void add_product(const float (*A)[kLd], const float (*B)[kLd],
-                                            float2 (&acc)[4][2])
+                                            float2 (&acc)[4][2], int k0 = 0, int k1 = kC)
 {
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
 #pragma unroll 4
-    for (int k = 0; k < kC; k += 4) {
+    for (int k = k0; k < k1; k += 4) {
         float4 a[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(&A[4 * ty + i][k]);
@@ -316,6 +316,8 @@ __global__ void __launch_bounds__(kThreads, 2) mix_simt_kernel(DecayShape S, Dec
     fetch_end();
     fetch_wait<1>();
     __syncthreads();
+    // a warp's eight rows and the keys on their side of the diagonal
+    const int r8 = 8 * (threadIdx.x >> 5), k0 = J.rev ? r8 : 0, k1 = J.rev ? kC : r8 + 8;
     float2 near[4][2] = {};
     for (int h = 0; h < nh; ++h) {
         float s[4][4];
@@ -334,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 2) mix_simt_kernel(DecayShape S, Dec
             fetch_tile(sm.Y, y + (h + 1) * next, c * kC, n);
             fetch_end();
         }
-        add_product(sm.P, sm.Z, near);
+        add_product(sm.P, sm.Z, near, k0, k1);
         if (h + 1 < nh) {
             fetch_wait<0>();
             __syncthreads();  // the next Y is there, Z and P are free
