@@ -231,24 +231,24 @@ struct MixSmem {
     float pw[kC + 1];  // powers of l
 };
 
-// s[i][e] = A[4 ty + i] . B[tx + 16 e]
+// s[i][e] = A[4 ty + i] . B[tx + 16 e], e < kE
+template <int kE>
 __device__ __forceinline__ void row_products(const float (*A)[kLd], const float (*B)[kLd],
-                                             float (&s)[4][4])
+                                             float (&s)[4][kE])
 {
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    float2 acc[4][4] = {};
+    float2 acc[4][kE] = {};
 #pragma unroll 4
     for (int k = 0; k < kD; k += 4) {
-        float4 a[4], b[4];
+        float4 a[4], b[kE];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            a[i] = *reinterpret_cast<const float4*>(&A[4 * ty + i][k]);
-            b[i] = *reinterpret_cast<const float4*>(&B[tx + 16 * i][k]);
-        }
+        for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(&A[4 * ty + i][k]);
+#pragma unroll
+        for (int e = 0; e < kE; ++e) b[e] = *reinterpret_cast<const float4*>(&B[tx + 16 * e][k]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
+            for (int e = 0; e < kE; ++e) {
                 acc[i][e] = __ffma2_rn(lo2(a[i]), lo2(b[e]), acc[i][e]);
                 acc[i][e] = __ffma2_rn(hi2(a[i]), hi2(b[e]), acc[i][e]);
             }
@@ -256,7 +256,24 @@ __device__ __forceinline__ void row_products(const float (*A)[kLd], const float 
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[i][e] = acc[i][e].x + acc[i][e].y;
+        for (int e = 0; e < kE; ++e) s[i][e] = acc[i][e].x + acc[i][e].y;
+}
+
+// Columns 16 e0 .. + 16 kE - 1 of P = (X Y^T) o D: all that a warp's rows read of it.
+template <int kE>
+__device__ __forceinline__ void decayed_scores(MixSmem& sm, int e0, int rev)
+{
+    const int ty = threadIdx.x >> 4, col0 = 16 * e0 + (threadIdx.x & 15);
+    float s[4][kE];
+    row_products<kE>(sm.X, sm.Y + 16 * e0, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int e = 0; e < kE; ++e) {
+            const int row = 4 * ty + i, col = col0 + 16 * e;
+            const int d = rev ? col - row : row - col;
+            sm.P[row][col] = d >= 0 ? s[i][e] * sm.pw[d] : 0.f;
+        }
 }
 
 // acc[i] += row 4 ty + i of A times B, columns 4 tx .. + 3, over k0 <= k < k1 (multiples of 4)
@@ -320,16 +337,14 @@ __global__ void __launch_bounds__(kThreads, 2) mix_simt_kernel(DecayShape S, Dec
     const int r8 = 8 * (threadIdx.x >> 5), k0 = J.rev ? r8 : 0, k1 = J.rev ? kC : r8 + 8;
     float2 near[4][2] = {};
     for (int h = 0; h < nh; ++h) {
-        float s[4][4];
-        row_products(sm.X, sm.Y, s);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int row = 4 * ty + i, col = tx + 16 * e;
-                const int d = J.rev ? col - row : row - col;
-                sm.P[row][col] = d >= 0 ? s[i][e] * sm.pw[d] : 0.f;
-            }
+        // blocks of 16 keys: the diagonal's and those on its side
+        const int at = threadIdx.x >> 6, e0 = J.rev ? at : 0;
+        switch (J.rev ? 4 - at : at + 1) {
+        case 1: decayed_scores<1>(sm, e0, J.rev); break;
+        case 2: decayed_scores<2>(sm, e0, J.rev); break;
+        case 3: decayed_scores<3>(sm, e0, J.rev); break;
+        default: decayed_scores<4>(sm, e0, J.rev);
+        }
         fetch_wait<0>();
         __syncthreads();  // P and Z (and M) are there, Y is free
         if (h + 1 < nh) {
@@ -347,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 2) mix_simt_kernel(DecayShape S, Dec
     float2 far[4][2] = {};
     if (J.mem_t) {
         float s[4][4];
-        row_products(sm.X, sm.M, s);
+        row_products<4>(sm.X, sm.M, s);
         __syncthreads();  // P is free
 #pragma unroll
         for (int i = 0; i < 4; ++i)
