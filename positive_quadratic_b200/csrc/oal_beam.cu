@@ -15,7 +15,9 @@
 //                        it, about n, are read again and their candidates ranked.  Scores are
 //                        compared in 64 bits: candidates of different rows may lie closer than
 //                        fp32 resolves.
-// The scan is bound by memory: 6 instructions per logit, 1/32 of the logits' count written.
+// The scan reads every logit once (128 rows of 151,936 in bf16, a fifth of them ended, 31 MB: 12 us,
+// 2.6 TB/s); the merge is a chain of dependent loads and barriers, 10 to 14 us whatever the size.  The
+// call takes 20.6 us there: the merge's launch is hidden behind the scan.
 #pragma once
 
 #include <cmath>
@@ -466,6 +468,7 @@ __global__ void __launch_bounds__(kMergeThreads, 1) select_merge_kernel(
 // ------------------------------------------------------------------------------------------
 // dst row i = src row parents[i], rows of `units` 16-byte words; block (part of a row, i).  The
 // last row of blocks copies the `head` words before the rows, with the batch size of dst.
+// Memory-bound: 64 states of 2 heads, 120 MB with the parents that are read, in 22.8 us, 5.3 TB/s.
 // ------------------------------------------------------------------------------------------
 constexpr int kCopy = 8;  // words in flight per thread
 
@@ -521,7 +524,9 @@ int tiles_of(int dtype, int V)
 }
 
 // Tiles per block of the scan: one, until the grid has four blocks for every SM (about as many as
-// are resident); then more, so that a block loads a tile while it works on the one before.
+// are resident); then more, so that a block loads a tile while it works on the one before.  128 rows
+// of 151,936 in bf16: 20.7 us, against 23.1 with three blocks per SM and 22.1 with eight (512 rows of
+// 32,000 in fp32: 26.1, and 25.2 with eight).
 int tiles_per_block(int rows, int all_tiles)
 {
     const long long tiles = (long long)rows * all_tiles, blocks = std::max(4 * sm_count(), 1);

@@ -40,7 +40,10 @@ __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 // ------------------------------------------------------------------------------------------
 // E_c of one (chunk, kv, b): a 64 x 64 product over the chunk's tokens, for every y head of the
 // kv head.  Thread (ty, tx) owns rows 4 ty .. + 3 and columns 4 tx .. + 3, in pairs of columns
-// (packed fp32 FMAs); the next head's tiles arrive while one is worked on.
+// (packed fp32 FMAs); the next head's tiles arrive while one is worked on.  The heads of a group are
+// summed in parts, a block each, where there are few chunks: the gradient of 4096 tokens of 14/2 heads
+// (1024 products of 64^3) takes 24 us, 22 TFLOP/s, and took 36 us with a group per block; 61 us on
+// single FMAs with tiles loaded in turn.
 // ------------------------------------------------------------------------------------------
 struct DeltaSmem {
     float Y[2][kC][kLd], Z[2][kC][kLd];
@@ -117,8 +120,11 @@ __global__ void __launch_bounds__(kThreads) delta_simt_kernel(DecayShape S, Deca
 // The scan over the chunks of every (b, kv): cur <- l^n cur + E_c, cur written before each.
 // Block = 32 kVec state entries (kVec per lane) and up to 64 chunks at a time, 8 per warp: a warp
 // sums its chunks by themselves, all of them loaded at once, then starts over from what the warps
-// before it leave.  One round trip to memory for 64 chunks instead of 64.  kVec = 2 gives twice
-// the blocks of kVec = 4, which matters where there are few planes.
+// before it leave.  One round trip to memory for 64 chunks instead of 64, and bound by it until
+// there are many planes: 64 planes of 64 chunks (100 MB) in 27 us, 3.7 TB/s.  kVec = 2 gives
+// twice the blocks of kVec = 4, which pays where there are few planes: both directions of 2 planes
+// of 32 chunks 8.6 us against 10.0 (one direction 6.7 against 6.9); 16 planes 12.8 against 10.7 and
+// 64 planes 31.9 against 27.7 are the other way round.
 // ------------------------------------------------------------------------------------------
 constexpr int kScanRun = 8;
 
@@ -224,7 +230,12 @@ __global__ void __launch_bounds__(kThreads) scan_kernel(DecayShape S, DecaySum a
 // ------------------------------------------------------------------------------------------
 // The mix of one (chunk, x head, b).  Thread (ty, tx) owns rows 4 ty .. + 3; of products of rows
 // (x . y) the columns tx + 16 e (conflict-free reads of y rows), of the output the columns
-// 4 tx .. + 3.  Packed fp32 FMAs; tiles arrive while others are worked on.
+// 4 tx .. + 3.  Packed fp32 FMAs; tiles arrive while others are worked on.  Of the products beyond
+// the diagonal each warp forms and uses those of its own rows' block alone.  Bound by the CUDA
+// cores, not by memory: 4096 tokens of 14/2 heads take 41 us (34 MB, 5 us of memory; 25 TFLOP/s of the
+// products formed), 49 us with the whole square, 75 us on single FMAs with tiles loaded in turn.
+// M in Y's place, for three blocks per SM, was slower where there are few items (2 x 1001 tokens of
+// 8 heads: a call of 28.8 us against 24.7).
 // ------------------------------------------------------------------------------------------
 struct MixSmem {
     float X[kC][kLd], Y[kC][kLd], Z[kC][kLd], M[kC][kLd], P[kC][kLd];
@@ -391,7 +402,10 @@ __global__ void __launch_bounds__(kThreads, 2) mix_simt_kernel(DecayShape S, Dec
 }
 
 // ------------------------------------------------------------------------------------------
-// One token: block = (kv, b).  Thread (r0, c4) holds rows r0 + 16 i of the columns 4 c4 .. + 3.
+// One token: block = (kv, b).  Thread (r0, c4) holds rows r0 + 16 i of the columns 4 c4 .. + 3.  The
+// state passes through registers once, all of it requested before anything is computed:
+// memory-bound, 1024 sequences of 16 heads (545 MB) in 84 us a call, 6.5 TB/s.  64 sequences of 2 heads
+// take 6 us, less than the host's call (10 us).
 // ------------------------------------------------------------------------------------------
 template <typename T>
 __global__ void __launch_bounds__(kThreads) step_kernel(const T* __restrict__ q,
@@ -471,7 +485,8 @@ int by_type(int dtype, F f)
 }
 
 // Parts in which the heads of a group are summed (the gradient's R): enough CTAs for two per SM
-// where the chunks alone are too few, at the price of a 16 KB partial sum each.
+// where the chunks alone are too few, at the price of a 16 KB partial sum each.  The gradient of 4096
+// tokens of 14/2 heads: 34.9 us with two per SM, 37.0 with three; in fp32 119 us, 131 without parts.
 constexpr int kSms = 148;
 int parts_of(const oal_shape* s, int grp)
 {

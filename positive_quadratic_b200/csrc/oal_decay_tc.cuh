@@ -120,7 +120,10 @@ __device__ __forceinline__ void zero_rows(unsigned char* tile, int n)
 // the state keeps fp32 accuracy.  Rows of the accumulator: [hi; mid] in one MMA group of M = 128
 // and [lo; hi] in a second, of which lo is used, so that E = hi + (mid + lo).
 // One CTA per (sum, part of the heads, b, kv, chunk); three fit an SM, since the high part is written
-// over y itself.
+// over y itself.  It does little with each byte (48 KB a chunk), and is bound by the row of latencies
+// from the copy over parts, products and tensor memory to the store, which the SM's other CTAs have to
+// cover: 4 x 8192 tokens of 16 heads (4096 chunks, 201 MB) take 60 us, 3.3 TB/s; with two CTAs per
+// SM it was 76 us.
 // ------------------------------------------------------------------------------------------
 struct SumMaps {
     CUtensorMap y[2], z[2];
@@ -318,6 +321,15 @@ __global__ void __launch_bounds__(kThreads, 3)
 // the next item's scores are formed while the compute warps write out the present one's result.
 // Warp 9 looks ahead: it works out the next items' places and powers of l and loads their tiles
 // as soon as buffers are free.
+// What bounds it is the chain of an item, about 4400 cycles from one to the next.  Measured parts:
+// Q K^T 650; scores to P 1000 to 1500 (the latencies of tensor-memory loads and stores: a block
+// behind the diagonal, a store alone, takes 430); P to the end of its products 900; from there to the
+// next item's first MMA 700.  Scores, U and F fill 256 columns, so two such chains run per SM, and
+// tensor memory has room for no third.
+// 8 x 4096 tokens of 14/2 heads: 45 us, of a call of 57 us whose 134 MB are 21 us of memory.  Tried and
+// not faster there (44 to 47 us at the time): 16 compute warps 48; two MMA warps taking turns 47; halves
+// of 64 keys, so that products and decays overlap, 57; rows stored straight from registers cost 1200
+// cycles an item in the shared-memory pipe.
 // ------------------------------------------------------------------------------------------
 struct MixJob {
     CUtensorMap x, y, z, m, o;
