@@ -466,11 +466,14 @@ int oal_beam_select_workspace_bytes(int B, int beams, int V, int n, int dtype, s
  *   scores [B][n] fp32, parents [B][n] int32 (rows of the B * beams, as oal_state_reorder and the
  *   beam steps take them), tokens [B][n] int32, best first.
  * The results must not overlap one another, running or ended (OAL_ERR_OVERLAP).
- * Equal scores come in the order of (row, token).  An ended row (ended[r] != 0) goes on with
+ * Equal scores come in the order of (row, token); rows of equal logits and equal running scores
+ * have equal scores.  An ended row (ended[r] != 0) goes on with
  * pad_token alone, at its running score, and its logits are not read.  A candidate that cannot
  * be (a logit of -inf; a row with a NaN or +inf logit, with no finite logit, or whose running
  * score is not finite; another token of an ended row) scores -inf, and is returned where no
- * others are left.  Scores are formed in 64 bits and rounded once.
+ * others are left.  Scores are formed and compared in 64 bits and rounded once to fp32.  A row's
+ * log sum of exponentials is made of fp32 exponentials, joined in 64 bits: it is right to 2^-17, mostly
+ * to 1e-7, and candidates of different rows that lie closer than that may come in either order.
  * n <= 32, n <= beams * V, beams <= 256, beams * V < 2^31 - 2^14, B * beams <= 65535. */
 int oal_beam_select(const void* logits, long long row_stride, int dtype, const float* running,
                     const uint8_t* ended, int pad_token, int B, int beams, int V, int n,

@@ -13,14 +13,19 @@
 //                        only bundles that reach it, a few n of them, have their groups looked
 //                        at; of these the n best give a better bound, and only groups that reach
 //                        it, about n, are read again and their candidates ranked.  Scores are
-//                        compared in 64 bits: candidates of different rows may lie closer than
-//                        fp32 resolves.
+//                        compared in 64 bits, so that a row's candidates keep the order of their
+//                        logits and those of different rows the order that the log-sums give them.
+// A log-sum is joined from fp32 exponentials in 64 bits.  With u = 2^-24: x - max, the factor log2 e
+// and their product are off by 2.5 u of a term's exponent d = max - x, ex2 by 4 u, and a thread's sum of
+// 32 terms by 10 u.  Terms weigh e^-d, so that the mean of d is below log V <= 21.5; with the
+// same for a partial sum that moves to a larger maximum: below 128 u = 2^-17 in all.
 // The scan reads every logit once (128 rows of 151,936 in bf16, a fifth of them ended, 31 MB: 12 us,
 // 2.6 TB/s); the merge is a chain of dependent loads and barriers, 10 to 14 us whatever the size.  The
 // call takes 20.6 us there: the merge's launch is hidden behind the scan.
 #pragma once
 
 #include <cmath>
+#include <type_traits>
 
 #include "oal_common.cuh"
 #include "oal_kernels.cuh"
@@ -64,15 +69,17 @@ __device__ __forceinline__ void unpack(uint4 a, float* x, __nv_bfloat16)
     }
 }
 
-// Where a row's groups lie.  A row need not start on 16 bytes: tile 0 starts at the aligned
-// address before it, and places outside the row count as absent.  Thread t of a tile holds
-// vectors of 16 bytes number i * 256 + t; element j of its group is at place_of(t, j).  Group
+// Where a row's groups lie.  Tiles, threads and partial sums follow the row's tokens, wherever the
+// row starts in memory: equal rows go through the same operations and have the same log-sum to the
+// last bit, so that their equal scores compare equal.  (Cut by 16-byte addresses, their log-sums
+// differed by about 1e-8, which decided the order.)  A warp of a tile has 1024 tokens in a row, as
+// vectors of 16 bytes; element j of the group of the tile's thread t is at place_of(t, j).  Group
 // tile * 256 + t of a row belongs to bundle (tile * 256 + t) / 32.
 template <typename T>
 __device__ __forceinline__ int place_of(int t, int j)
 {
     constexpr int kN = VecOf<T>::n;
-    return ((j / kN) * kThreads + t) * kN + j % kN;
+    return ((t / 32 * (kGroup / kN) + j / kN) * 32 + t % 32) * kN + j % kN;
 }
 
 // Floats in the order of unsigned integers, and back.
@@ -95,8 +102,11 @@ __device__ __forceinline__ float exp2_fast(float x)
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Block (slice, row): `tiles` tiles from slice * tiles on.  gmax [rows][all tiles][256], bmax
-// [rows][all tiles][8].
-template <typename T>
+// [rows][all tiles][8].  kSkew: rows need not start on 16 bytes; their vectors are put together from
+// the aligned ones that a lane and its neighbour hold.  128 rows of 50,257: a call of 15.8 us in bf16
+// and 17.6 in fp32, against 15.4 and 16.4 when rows were cut by address; 128 rows of 151,936 in bf16,
+// which start on 16 bytes: 21.4.
+template <typename T, bool kSkew>
 __global__ void __launch_bounds__(kThreads) select_scan_kernel(
     const T* __restrict__ logits, long long ld, int rows, int V, int tiles, int all_tiles,
     const float* __restrict__ running, const uint8_t* __restrict__ ended,
@@ -108,39 +118,67 @@ __global__ void __launch_bounds__(kThreads) select_scan_kernel(
     // the merge does not look at such a row's groups
     if ((ended && ended[row]) || !isfinite(running[row])) return;
     const long long first = row * ld;
-    const int skew = int(first % kN);
+    const int skew = kSkew ? int(first % kN) : 0;
     const long long end = (rows - 1) * ld + V;  // of the whole array
+    // tokens of this row from here on lie in the array's last vector, which `end` cuts short
+    const int cut = max(int(min(end - end % kN - first, (long long)V)), 0);
     const int t_first = blockIdx.x * tiles, t_last = min(t_first + tiles, all_tiles);
     float m = -INFINITY;   // this thread's maximum, and its sum of exp(x - m)
     double s = 0.0;
     bool nan = false;
-    uint4 raw[kVecs];
+    uint4 raw[kVecs], behind;  // behind: the vector after the warp's (lane 0)
+    auto vector = [&](long long at) {
+        return at + kN <= end ? __ldcs(reinterpret_cast<const uint4*>(logits + at))
+                              : make_uint4(0, 0, 0, 0);
+    };
     auto load = [&](int tile) {
-        const long long base = first - skew + (long long)tile * kTile;
+        const long long at = first - skew + (long long)tile * kTile + place_of<T>(tid, 0);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) {
-            const long long at = base + (long long)(i * kThreads + tid) * kN;
-            raw[i] = at + kN <= end ? __ldcs(reinterpret_cast<const uint4*>(logits + at))
-                                    : make_uint4(0, 0, 0, 0);
-        }
+        for (int i = 0; i < kVecs; ++i) raw[i] = vector(at + i * 32 * kN);
+        if (kSkew && lane == 0) behind = vector(at + kVecs * 32 * kN);
     };
     load(t_first);
     for (int tile = t_first; tile < t_last; ++tile) {
         float x[kGroup];
+        if (kSkew) {
+            // the row's vectors start kW words (and half a word, in bf16) into the aligned ones
+            auto unpack_from = [&](auto words) {
+                constexpr int kW = decltype(words)::value, kHalf = sizeof(T) == 2;
+                const int half = kHalf ? 16 * (skew & 1) : 0;
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i) unpack(raw[i], x + i * kN, T());
-        const int t0 = tile * kTile - skew;  // token of the tile's place 0
-        const bool edge = t0 < 0 || t0 + kTile > V;
-        if (edge) {
-            // the last vector of the array may be cut short, and tokens may lie outside the row
-            const long long base = first - skew + (long long)tile * kTile;
+                for (int i = 0; i < kVecs; ++i) {
+                    const uint4 a = raw[i], last = i + 1 < kVecs ? raw[(i + 1) % kVecs] : behind;
+                    uint32_t w[8] = {a.x, a.y, a.z, a.w, last.x, last.y, last.z, last.w}, v[4];
 #pragma unroll
-            for (int j = 0; j < kGroup; ++j) {
-                const int place = place_of<T>(tid, j);
-                if (j % kN == 0 && base + place < end && base + place + kN > end)
-                    for (int e = 0; e < kN; ++e)
-                        x[j + e] = base + place + e < end ? to_f32(logits[base + place + e]) : 0.f;
-                if (unsigned(t0 + place) >= unsigned(V)) x[j] = -INFINITY;
+                    for (int e = 0; e < kW + kHalf; ++e)  // lane 31's neighbour: lane 0's next vector
+                        w[4 + e] = __shfl_sync(~0u, lane == 0 ? w[4 + e] : w[e], (lane + 1) & 31);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        v[e] = kHalf ? __funnelshift_r(w[kW + e], w[kW + e + kHalf], half) : w[kW + e];
+                    unpack(make_uint4(v[0], v[1], v[2], v[3]), x + i * kN, T());
+                }
+            };
+            switch (skew * int(sizeof(T)) / 4) {
+            case 0: unpack_from(std::integral_constant<int, 0>{}); break;
+            case 1: unpack_from(std::integral_constant<int, 1>{}); break;
+            case 2: unpack_from(std::integral_constant<int, 2>{}); break;
+            default: unpack_from(std::integral_constant<int, 3>{});
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i) unpack(raw[i], x + i * kN, T());
+        }
+        const int t0 = tile * kTile;  // token of the tile's place 0
+        if (t0 + kTile > cut) {
+#pragma unroll
+            for (int j = 0; j < kGroup; ++j)
+                if (t0 + place_of<T>(tid, j) >= V) x[j] = -INFINITY;
+#pragma unroll 1
+            for (int t = max(cut, t0); t < min(V, t0 + kTile); ++t) {
+                const float one = to_f32(logits[first + t]);
+#pragma unroll
+                for (int j = 0; j < kGroup; ++j)
+                    if (t0 + place_of<T>(tid, j) == t) x[j] = one;
             }
         }
         if (tile + 1 < t_last) load(tile + 1);
@@ -210,7 +248,6 @@ __global__ void __launch_bounds__(kMergeThreads, 1) select_merge_kernel(
     const float* __restrict__ running, const uint8_t* __restrict__ ended, int pad_token,
     float* __restrict__ scores, int32_t* __restrict__ parents, int32_t* __restrict__ tokens)
 {
-    constexpr int kN = VecOf<T>::n;
     const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row0 = b * beams;
     // of each row its running score, its largest logit and log sum exp(x - max): apart, since a
@@ -368,11 +405,9 @@ __global__ void __launch_bounds__(kMergeThreads, 1) select_merge_kernel(
     have = groups;
     // A group's logits, one per lane; `keep` says which count.
     auto expand = [&](int r, int g, auto keep) {
-        const long long first = (row0 + r) * ld;
-        const int skew = int(first % kN), tile = g / kThreads;
-        const int t = tile * kTile - skew + place_of<T>(g % kThreads, lane);
-        if (unsigned(t) < unsigned(V)) {
-            const float x = to_f32(logits[first + t]);
+        const int t = g / kThreads * kTile + place_of<T>(g % kThreads, lane);
+        if (t < V) {
+            const float x = to_f32(logits[(row0 + r) * ld + t]);
             const double v = x > -INFINITY ? score(r, x) : -INFINITY;
             if (keep(v) && v > -INFINITY) {
                 const int i = atomicAdd(&found, 1);
@@ -403,10 +438,9 @@ __global__ void __launch_bounds__(kMergeThreads, 1) select_merge_kernel(
                 if (!__syncthreads_or(v >= bound)) continue;
                 // the tile's logits in the order of their places, 1024 at a time
                 const long long first = (row0 + r) * ld;
-                const int t0 = tile * kTile - int(first % kN);
                 for (int at = 0; at < kTile && ties < n; at += kMergeThreads) {
-                    const int t = t0 + at + tid;
-                    const bool hit = unsigned(t) < unsigned(V) &&
+                    const int t = tile * kTile + at + tid;
+                    const bool hit = t < V &&
                                      score(r, to_f32(logits[first + t])) == bound;
                     const uint32_t in_warp = __ballot_sync(~0u, hit);
                     __shared__ int before[kMergeWarps];
@@ -517,11 +551,7 @@ int gather_rows(const void* src, int src_rows, const int32_t* parents, void* dst
     return OAL_OK;
 }
 
-// Tiles of a row; a misaligned row needs up to a vector more.
-int tiles_of(int dtype, int V)
-{
-    return (V + (dtype == OAL_BF16 ? 7 : 3) + kTile - 1) / kTile;
-}
+int tiles_of(int V) { return (V + kTile - 1) / kTile; }
 
 // Tiles per block of the scan: one, until the grid has four blocks for every SM (about as many as
 // are resident); then more, so that a block loads a tile while it works on the one before.  128 rows
@@ -536,9 +566,9 @@ int tiles_per_block(int rows, int all_tiles)
 struct SelectLayout {
     size_t gmax, bmax, total;  // the slices' sums lie before the maxima
 };
-SelectLayout select_layout(int dtype, int rows, int V)
+SelectLayout select_layout(int rows, int V)
 {
-    const size_t tiles = size_t(rows) * tiles_of(dtype, V);  // at least as many as slices
+    const size_t tiles = size_t(rows) * tiles_of(V);  // at least as many as slices
     SelectLayout l;
     l.gmax = align256(tiles * sizeof(Slice));
     l.bmax = l.gmax + tiles * kThreads * sizeof(float);
@@ -546,7 +576,7 @@ SelectLayout select_layout(int dtype, int rows, int V)
     return l;
 }
 
-// (A tile may reach past the last logit, by less than two tiles: its places stay below 2^31.)
+// (A tile may reach past the last logit, by less than a tile: its places stay below 2^31.)
 int check_select(int B, int beams, int V, int n, int dtype)
 {
     if (B < 0 || beams < 1 || V < 1 || n < 1) return OAL_ERR_SHAPE;
@@ -564,18 +594,18 @@ cudaError_t launch_select(const void* logits, long long ld, const float* running
                           float* scores, int32_t* parents, int32_t* tokens, void* ws,
                           cudaStream_t st)
 {
-    constexpr int dtype = sizeof(T) == 2 ? OAL_BF16 : OAL_F32;
-    const int rows = B * beams, all_tiles = tiles_of(dtype, V);
+    const int rows = B * beams, all_tiles = tiles_of(V);
     const int tiles = tiles_per_block(rows, all_tiles), slices = (all_tiles + tiles - 1) / tiles;
     Slice* part = static_cast<Slice*>(ws);
-    const SelectLayout l = select_layout(dtype, rows, V);
+    const SelectLayout l = select_layout(rows, V);
     float* gmax = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + l.gmax);
     float* bmax = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + l.bmax);
     const T* x = static_cast<const T*>(logits);
     {
         LaunchScope ls("select_scan", st);
-        select_scan_kernel<T><<<dim3(slices, rows), kThreads, 0, st>>>(
-            x, ld, rows, V, tiles, all_tiles, running, ended, gmax, bmax, part);
+        const auto scan = ld % VecOf<T>::n ? select_scan_kernel<T, true> : select_scan_kernel<T, false>;
+        scan<<<dim3(slices, rows), kThreads, 0, st>>>(x, ld, rows, V, tiles, all_tiles, running, ended,
+                                                      gmax, bmax, part);
         const cudaError_t e = cudaGetLastError();
         if (e != cudaSuccess) return e;
     }
@@ -614,7 +644,7 @@ int oal_beam_select_workspace_bytes(int B, int beams, int V, int n, int dtype, s
     const int rc = beam::check_select(B, beams, V, n, dtype);
     if (rc) return rc;
     if (!bytes) return OAL_ERR_NULL;
-    *bytes = beam::select_layout(dtype, B * beams, V).total;
+    *bytes = beam::select_layout(B * beams, V).total;
     return OAL_OK;
 }
 

@@ -342,3 +342,27 @@ def test_binding_refusals(cuda):
         oal.state_reorder(src, par.long(), src.clone(), 2, 1)
     with pytest.raises(oal.OALError):
         oal.state_reorder(src, par, src, 2, 1)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("V", [1, 7, 1001, 9001, 50257, 250002])
+@pytest.mark.parametrize("gap", [0, 1, 6])
+def test_select_equal_rows(cuda, dtype, V, gap):
+    """Rows of equal logits and running scores tie for every token, wherever they start in memory
+    (V + gap is no multiple of a 16-byte vector), and n cuts through a tie."""
+    wide = torch.zeros(2, 5, V + gap, dtype=dtype, device=cuda)
+    x = wide[:, :, :V]
+    x.copy_(make(cuda, 2, 1, V, dtype)[0].expand(2, 5, V))
+    x[:, 2] = make(cuda, 2, 1, V, dtype, seed=1)[0][:, 0]
+    run = torch.tensor([[-3.3] * 5, [-0.7, -0.7, -9.0, -0.7, -0.7]], device=cuda)
+    for n in (2, 6, 11):
+        if n <= 5 * V:
+            check_select(x, run, n)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("beams", [1, 3, 5])
+def test_select_of_rows_that_end_inside_a_vector(cuda, dtype, beams):
+    """The array's last vector holds tokens of one row or two, of one tile or two."""
+    for V in [*range(1, 12), *range(8185, 8200), *range(16384, 16392)]:
+        check_select(*make(cuda, 1, beams, V, dtype), min(4, beams * V))
