@@ -465,7 +465,8 @@ int oal_beam_select_workspace_bytes(int B, int beams, int V, int n, int dtype, s
  *   first 16-byte aligned; running [B * beams] fp32; ended [B * beams] bytes, or NULL;
  *   scores [B][n] fp32, parents [B][n] int32 (rows of the B * beams, as oal_state_reorder and the
  *   beam steps take them), tokens [B][n] int32, best first.
- * The results must not overlap one another, running or ended (OAL_ERR_OVERLAP).
+ * The results must not overlap one another, running, ended or the logits, the space between their
+ * rows included (OAL_ERR_OVERLAP).
  * Equal scores come in the order of (row, token); rows of equal logits and equal running scores
  * have equal scores.  An ended row (ended[r] != 0) goes on with
  * pad_token alone, at its running score, and its logits are not read.  A candidate that cannot

@@ -668,9 +668,11 @@ int oal_beam_select(const void* logits, long long row_stride, int dtype, const f
     if ((rc = oal_beam_select_workspace_bytes(B, beams, V, n, dtype, &need))) return rc;
     if (!workspace || workspace_bytes < need) return OAL_ERR_WORKSPACE;
     if (!aligned16(workspace)) return OAL_ERR_ALIGN;
-    const size_t n_out = size_t(B) * n * 4;
+    // (one search's block may write its results while another's reads its logits again)
+    const size_t n_out = size_t(B) * n * 4, rows = size_t(B) * beams;
+    const size_t n_in = ((rows - 1) * size_t(row_stride) + V) * (dtype == OAL_BF16 ? 2 : 4);
     if (any_overlap({{scores, n_out}, {parents, n_out}, {tokens, n_out}},
-                    {{running, size_t(B) * beams * 4}, {ended, size_t(B) * beams}}))
+                    {{logits, n_in}, {running, rows * 4}, {ended, rows}}))
         return OAL_ERR_OVERLAP;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const auto go = dtype == OAL_BF16 ? beam::launch_select<__nv_bfloat16>

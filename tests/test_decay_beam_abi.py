@@ -285,3 +285,12 @@ def test_binding_refuses_host_tensors():
                  lambda: oal.decode_step_beam(q, k, k, buf, i32, buf.clone(), buf)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_select_over_its_logits(L):
+    """Results anywhere from the first logit of the first row to the last one of the last."""
+    at = apart("logits", "running", "ended", "scores", "parents", "tokens", "ws")
+    last = at["logits"] + 2 * (7 * 1004 + 1000) - 4  # 8 rows of 1000 bf16, 1004 apart
+    for w in ("scores", "parents", "tokens"):
+        for place in (at["logits"], at["logits"] + 4000, last, at["logits"] - 4):
+            assert select(L, ld=1004, **ptrs({**at, w: place})) == OVERLAP, (w, place)
