@@ -433,8 +433,8 @@ int oal_decay_prefill_continue(const void* q, const void* k, const void* v,
 /* One token for every sequence (T of `s` is not used): q [B][Hq][1][64], k, v [B][Hkv][1][64],
  * out [B][Hq][1][64].  With src == NULL `state` is updated in place.  With src (src_B sequences)
  * and parents [B] int32 on the device, sequence b goes on from sequence parents[b] of src, and
- * `state` receives the result: a beam search's reordering and step in one pass.  src and state
- * must not overlap (OAL_ERR_OVERLAP); the same parent may be named any number of times; one out
+ * `state` receives the result: a beam search's reordering and step in one pass.  src must not
+ * overlap state or out (OAL_ERR_OVERLAP); the same parent may be named any number of times; one out
  * of range sets OAL_ERR_VALUE and is clamped.  Memory-bound: the state is read and written once. */
 int oal_decay_step(const void* q, const void* k, const void* v, const float* log_decay,
                    float scale, const float* src, int src_B, const int32_t* parents, float* state,

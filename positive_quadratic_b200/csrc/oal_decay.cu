@@ -743,16 +743,16 @@ int oal_decay_step(const void* q, const void* k, const void* v, const float* log
     if (!aligned16(state) || !aligned16(src) || (reinterpret_cast<uintptr_t>(log_decay) & 3) ||
         (reinterpret_cast<uintptr_t>(parents) & 3))
         return OAL_ERR_ALIGN;
+    oal_shape from = one;
     if (src) {
         if (src_B < 1) return OAL_ERR_SHAPE;
-        oal_shape from = one;
         from.B = src_B;
         if ((rc = check_common(&from))) return rc;
-        if (overlap(src, decay::state_bytes(&from), state, decay::state_bytes(s)))
-            return OAL_ERR_OVERLAP;
     }
     const size_t nq = decay::io_bytes(&one, s->Hq), nk = decay::io_bytes(&one, s->Hkv);
-    if (any_overlap({{out, nq}, {state, decay::state_bytes(s)}}, {{q, nq}, {k, nk}, {v, nk}}))
+    if (any_overlap({{out, nq}, {state, decay::state_bytes(s)}},
+                    {{q, nq}, {k, nk}, {v, nk}, {log_decay, size_t(s->Hkv) * 4},
+                     {src, decay::state_bytes(&from)}, {parents, size_t(s->B) * 4}}))
         return OAL_ERR_OVERLAP;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return decay::by_type(s->dtype, [&](auto t) {

@@ -294,3 +294,17 @@ def test_select_over_its_logits(L):
     for w in ("scores", "parents", "tokens"):
         for place in (at["logits"], at["logits"] + 4000, last, at["logits"] - 4):
             assert select(L, ld=1004, **ptrs({**at, w: place})) == OVERLAP, (w, place)
+
+
+def test_step_from_parents_over_its_inputs(L):
+    s = shape(T=1)
+    at = apart("q", "k", "v", "g", "src", "parents", "state", "out")
+
+    def call(**kw):
+        a = ptrs({**at, **kw})
+        return L.oal_decay_step(a["q"], a["k"], a["v"], a["g"], SCALE, a["src"], 3, a["parents"],
+                                a["state"], a["out"], ctypes.byref(s), None)
+
+    last = at["src"] + 3 * 2 * 16384 - 16
+    for place in (at["src"], last, at["g"], at["parents"]):
+        assert call(out=place) == OVERLAP and call(state=place) == OVERLAP, place
