@@ -797,9 +797,12 @@ int oal_decay_backward(const void* q, const void* k, const void* v, const float*
     if (!aligned16(workspace)) return OAL_ERR_ALIGN;
     const size_t nq = decay::io_bytes(s, s->Hq), nk = decay::io_bytes(s, s->Hkv);
     const size_t ns = decay::state_bytes(s);
+    // (dstate over dlast itself: the block that writes an entry has read it before)
     if (any_overlap({{dq, nq}, {dk, nk}, {dv, nk}, {dstate, ns}},
-                    {{q, nq}, {k, nk}, {v, nk}, {dout, nq}, {state, ns}}) ||
-        (dstate != dlast && dstate && dlast && overlap(dstate, ns, dlast, ns)))
+                    {{q, nq}, {k, nk}, {v, nk}, {dout, nq}, {state, ns},
+                     {log_decay, size_t(s->Hkv) * 4}, {lens, size_t(s->B) * 4}}) ||
+        any_overlap({{dq, nq}, {dk, nk}, {dv, nk}, {dstate == dlast ? nullptr : dstate, ns}},
+                    {{dlast, ns}}))
         return OAL_ERR_OVERLAP;
     OAL_CUDA_TRY(decay::set_attributes_once());
     const DecayShape S{s->B, s->T, s->Hkv, decay::chunks_of(s), lens, log_decay, scale};

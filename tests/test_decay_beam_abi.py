@@ -308,3 +308,23 @@ def test_step_from_parents_over_its_inputs(L):
     last = at["src"] + 3 * 2 * 16384 - 16
     for place in (at["src"], last, at["g"], at["parents"]):
         assert call(out=place) == OVERLAP and call(state=place) == OVERLAP, place
+
+
+def test_backward_over_the_last_state_gradient(L):
+    """Every gradient but dstate, which may be dlast itself; and the decays and lengths."""
+    s = shape()
+    at = apart("q", "k", "v", "g", "lens", "dout", "state", "dlast", "dq", "dk", "dv", "dstate", "ws")
+
+    def call(**kw):
+        a = ptrs({**at, **kw})
+        return L.oal_decay_backward(
+            a["q"], a["k"], a["v"], a["g"], SCALE, a["lens"], a["dout"], a["state"], a["dlast"],
+            a["dq"], a["dk"], a["dv"], a["dstate"], a["ws"], BIG, ctypes.byref(s), None)
+
+    for w in ("dq", "dk", "dv"):
+        for place in (at["dlast"], at["dlast"] + 2 * 2 * 16384 - 16):
+            assert call(**{w: place}) == OVERLAP, w
+    for w in ("dq", "dk", "dv", "dstate"):
+        for r in ("g", "lens"):
+            assert call(**{w: at[r]}) == OVERLAP, (w, r)
+    assert call(dstate=at["dlast"] + 16) == OVERLAP
