@@ -496,7 +496,8 @@ int oal_decay_state_reorder(const float* src, int src_B, const int32_t* parents,
 
 /* oal_decode_step of sequence b from sequence parents[b] of `src`, into `dst`: the result of
  * oal_state_reorder followed by oal_decode_step, bit for bit, in one pass over the states
- * instead of two.  Arguments as for those two; src is left as it was. */
+ * instead of two.  Arguments as for those two; src is left as it was.  dst and out must not overlap
+ * the inputs or one another (OAL_ERR_OVERLAP). */
 int oal_decode_step_beam(const void* q, const void* k, const void* v, const void* src, int src_B,
                          const int32_t* parents, void* dst, float* out, void* workspace,
                          size_t workspace_bytes, const oal_shape* s, void* stream);

@@ -720,8 +720,11 @@ int oal_decode_step_beam(const void* q, const void* k, const void* v, const void
     oal_decode_workspace_bytes(s, &need);
     if (!workspace || workspace_bytes < need) return OAL_ERR_WORKSPACE;
     if (!aligned16(workspace)) return OAL_ERR_ALIGN;
-    if (overlap(src, state_bytes(src_B, s->Hq, s->Hkv), dst,
-                      state_bytes(s->B, s->Hq, s->Hkv)))
+    const size_t token = size_t(s->B) * kD, nq = token * s->Hq, nk = token * s->Hkv;
+    const size_t es = s->dtype == OAL_BF16 ? 2 : 4;
+    if (any_overlap({{dst, state_bytes(s->B, s->Hq, s->Hkv)}, {out, nq * sizeof(float)}},
+                    {{src, state_bytes(src_B, s->Hq, s->Hkv)}, {q, nq * es}, {k, nk * es},
+                     {v, nk * es}, {parents, size_t(s->B) * 4}}))
         return OAL_ERR_OVERLAP;
     if (s->B == 0) return oal_state_reorder(src, src_B, parents, dst, s, stream);  // tables alone
     return launch_decode(q, k, v, dst, out,

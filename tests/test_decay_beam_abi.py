@@ -328,3 +328,22 @@ def test_backward_over_the_last_state_gradient(L):
         for r in ("g", "lens"):
             assert call(**{w: at[r]}) == OVERLAP, (w, r)
     assert call(dstate=at["dlast"] + 16) == OVERLAP
+
+
+def test_decode_step_beam_over_its_inputs(L):
+    s = shape(B=3, T=1)
+    at = apart("q", "k", "v", "src", "parents", "dst", "out", "ws")
+    ends = {"src": oal.state_bytes(shape(B=4, T=1)), "dst": oal.state_bytes(s), "q": 3 * 4 * 64 * 2,
+            "k": 3 * 2 * 64 * 2, "v": 3 * 2 * 64 * 2}
+
+    def call(**kw):
+        a = ptrs({**at, **kw})
+        return L.oal_decode_step_beam(a["q"], a["k"], a["v"], a["src"], 4, a["parents"], a["dst"],
+                                      a["out"], a["ws"], BIG, ctypes.byref(s), None)
+
+    for r, size in ends.items():
+        for place in (at[r], at[r] + size - 16):
+            assert call(out=place) == OVERLAP, r
+            if r != "dst":
+                assert call(dst=place) == OVERLAP, r
+    assert call(out=at["parents"]) == OVERLAP and call(dst=at["parents"]) == OVERLAP
