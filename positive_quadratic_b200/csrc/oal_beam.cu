@@ -687,8 +687,8 @@ int oal_state_reorder(const void* src, int src_B, const int32_t* parents, void* 
 {
     int rc = beam::check_reorder(src, src_B, parents, dst, s);
     if (rc) return rc;
-    if (overlap(src, state_bytes(src_B, s->Hq, s->Hkv), dst,
-                      state_bytes(s->B, s->Hq, s->Hkv)))
+    if (any_overlap({{dst, state_bytes(s->B, s->Hq, s->Hkv)}},
+                    {{src, state_bytes(src_B, s->Hq, s->Hkv)}, {parents, size_t(s->B) * 4}}))
         return OAL_ERR_OVERLAP;
     return beam::gather_rows(src, src_B, parents, dst, s->B, size_t(s->Hkv) * state_unit_bytes(),
                              kHeaderBytes + coef_bytes(s->Hq), static_cast<cudaStream_t>(stream));
@@ -700,7 +700,8 @@ int oal_decay_state_reorder(const float* src, int src_B, const int32_t* parents,
     int rc = beam::check_reorder(src, src_B, parents, dst, s);
     if (rc) return rc;
     const size_t row = size_t(s->Hkv) * kD * kDV * 4;
-    if (overlap(src, src_B * row, dst, s->B * row)) return OAL_ERR_OVERLAP;
+    if (any_overlap({{dst, s->B * row}}, {{src, src_B * row}, {parents, size_t(s->B) * 4}}))
+        return OAL_ERR_OVERLAP;
     if (s->B == 0) return OAL_OK;
     return beam::gather_rows(src, src_B, parents, dst, s->B, row, 0,
                              static_cast<cudaStream_t>(stream));

@@ -670,10 +670,12 @@ int prefill(const void* q, const void* k, const void* v, const float* log_decay,
     if ((rc = oal_decay_prefill_workspace_bytes(s, &need))) return rc;
     if (!ws || ws_bytes < need) return OAL_ERR_WORKSPACE;
     if (!aligned16(ws)) return OAL_ERR_ALIGN;
+    if (cont && s->T == 0) return OAL_OK;  // nothing is written
     const size_t nq = io_bytes(s, s->Hq), nk = io_bytes(s, s->Hkv);
-    if (any_overlap({{out, nq}, {state, state_bytes(s)}}, {{out ? q : nullptr, nq}, {k, nk}, {v, nk}}))
+    if (any_overlap({{out, nq}, {state, state_bytes(s)}},
+                    {{out ? q : nullptr, nq}, {k, nk}, {v, nk}, {log_decay, size_t(s->Hkv) * 4},
+                     {lens, size_t(s->B) * 4}}))
         return OAL_ERR_OVERLAP;
-    if (cont && s->T == 0) return OAL_OK;
     OAL_CUDA_TRY(set_attributes_once());
     const DecayShape S{s->B, s->T, s->Hkv, chunks_of(s), lens, log_decay, scale};
     cudaStream_t st = static_cast<cudaStream_t>(stream);

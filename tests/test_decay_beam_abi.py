@@ -347,3 +347,20 @@ def test_decode_step_beam_over_its_inputs(L):
             if r != "dst":
                 assert call(dst=place) == OVERLAP, r
     assert call(out=at["parents"]) == OVERLAP and call(dst=at["parents"]) == OVERLAP
+
+
+@pytest.mark.parametrize("fn", ["oal_decay_prefill", "oal_decay_prefill_continue"])
+def test_prefill_over_decays_and_lengths(L, fn):
+    at = apart("q", "k", "v", "g", "lens", "out", "state", "ws")
+    for w in ("out", "state"):
+        for r in ("g", "lens"):
+            assert call_prefill(L, shape(), fn, **ptrs({**at, w: at[r]})) == OVERLAP, (w, r)
+
+
+def test_reorder_over_its_indices(L):
+    s = shape(B=3)
+    at = ptrs(apart("src", "parents", "dst"))
+    for fn in ("oal_state_reorder", "oal_decay_state_reorder"):
+        assert getattr(L, fn)(at["src"], 3, at["dst"], at["dst"], ctypes.byref(s), None) == OVERLAP
+        inside = P(at["dst"].value + 3 * 2 * 16384 - 4)
+        assert getattr(L, fn)(at["src"], 3, inside, at["dst"], ctypes.byref(s), None) == OVERLAP
