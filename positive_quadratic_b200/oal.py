@@ -628,7 +628,6 @@ def _call_on_stream(f):
     makes belong to that stream, and their memory is not handed out again before the call's
     kernels are done with it."""
     first = f.__code__.co_varnames[0]
-    device, raw = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
     @functools.wraps(f)
     def call(*args, stream=None, **kwargs):
@@ -636,10 +635,11 @@ def _call_on_stream(f):
         index = x.get_device()
         if index < 0:
             raise ValueError("tensors must be contiguous CUDA tensors")
-        if stream is None and index == device():
-            return f(*args, stream=raw(index), **kwargs)
+        torch_c = torch._C  # (a torch without CUDA lacks the two functions)
+        if stream is None and index == torch_c._cuda_getDevice():
+            return f(*args, stream=torch_c._cuda_getCurrentRawStream(index), **kwargs)
         with _There(x.device, stream):
-            return f(*args, stream=raw(index), **kwargs)
+            return f(*args, stream=torch_c._cuda_getCurrentRawStream(index), **kwargs)
     return call
 
 

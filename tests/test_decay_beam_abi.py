@@ -1,6 +1,9 @@
 """Host-side checks of decayed linear attention, beam selection and state reordering: every refusal
 comes before the device is touched, so these run without a GPU."""
 import ctypes
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -364,3 +367,24 @@ def test_reorder_over_its_indices(L):
         assert getattr(L, fn)(at["src"], 3, at["dst"], at["dst"], ctypes.byref(s), None) == OVERLAP
         inside = P(at["dst"].value + 3 * 2 * 16384 - 4)
         assert getattr(L, fn)(at["src"], 3, inside, at["dst"], ctypes.byref(s), None) == OVERLAP
+
+
+def test_binding_loads_on_a_torch_without_cuda():
+    """Size queries and refusals work there."""
+    code = """
+import torch
+for name in ("_cuda_getDevice", "_cuda_getCurrentRawStream"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from positive_quadratic_b200 import oal
+assert oal.state_bytes(oal.make_shape(1, 1, 2, 1)) > 0
+x = torch.zeros(1, 1, 1, 64)
+try:
+    oal.decay_step(x, x, x, torch.zeros(1), 0.1, torch.zeros(1, 1, 64, 64))
+except ValueError as e:
+    assert "CUDA" in str(e)
+else:
+    raise AssertionError("a host tensor passed")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(oal.__file__)))
+    subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
