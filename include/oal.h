@@ -484,7 +484,8 @@ int oal_beam_select(const void* logits, long long row_stride, int dtype, const f
 /* Copies prefix states: sequence b of `dst` (a state buffer of `s`) becomes sequence parents[b]
  * of `src` (a state buffer of src_B sequences, the same Hq and Hkv).  Header and coefficient
  * tables are copied too, so dst needs no initialisation, and s->B may differ from src_B (a
- * prompt's state spread over its beams).  parents [B] int32 on the device; the same parent may
+ * prompt's state spread over its beams).  A buffer that was made for more sequences holds those that
+ * its header names: the smaller of the two counts.  parents [B] int32 on the device; the same parent may
  * be named any number of times; one out of range sets OAL_ERR_VALUE and is clamped.  dst must not
  * overlap src or parents (OAL_ERR_OVERLAP). */
 int oal_state_reorder(const void* src, int src_B, const int32_t* parents, void* dst,

@@ -522,6 +522,7 @@ __global__ void __launch_bounds__(kThreads) gather_rows_kernel(const uint4* __re
         return;
     }
     int from = parents[i];
+    if (head) src_rows = state_sequences(src, src_rows);  // a buffer may have room for more
     if (from < 0 || from >= src_rows) {
         if (threadIdx.x == 0) raise_error(OAL_ERR_VALUE);
         from = from < 0 ? 0 : src_rows - 1;

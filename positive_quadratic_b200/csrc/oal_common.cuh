@@ -66,6 +66,13 @@ struct StateHeader {
 };
 static_assert(sizeof(StateHeader) == kHeaderBytes, "header must be 256 bytes");
 
+// Sequences that a quadratic state holds: as many as its header says, of a buffer with room for
+// `room` (>= 1).  At least 1, whatever the header holds, as an index is clamped to it.
+__device__ __forceinline__ int state_sequences(const void* state, int room)
+{
+    return max(min(static_cast<const StateHeader*>(state)->B, room), 1);
+}
+
 __host__ __device__ constexpr size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 __host__ __device__ constexpr size_t coef_bytes(int Hq) { return align256(size_t(Hq) * kFP * 4); }
 __host__ __device__ constexpr size_t state_unit_bytes() { return size_t(kFP) * kW * 4; }

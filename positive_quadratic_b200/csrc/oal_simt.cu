@@ -499,9 +499,10 @@ __global__ void __launch_bounds__(kDecThreads, 4) decode_kernel(const Tin* __res
     const float* unit_in = unit;
     if constexpr (kBeam) {
         int from = parents[b];
-        if (from < 0 || from >= src_B) {
+        const int held = state_sequences(src, src_B);
+        if (from < 0 || from >= held) {
             if (tid == 0) raise_error(OAL_ERR_VALUE);
-            from = from < 0 ? 0 : src_B - 1;
+            from = from < 0 ? 0 : held - 1;
         }
         unit_in = reinterpret_cast<const float*>(src + kHeaderBytes + coef_bytes(Hq)) +
                   (size_t(from) * Hkv + kv) * kFP * kW;

@@ -366,3 +366,31 @@ def test_select_of_rows_that_end_inside_a_vector(cuda, dtype, beams):
     """The array's last vector holds tokens of one row or two, of one tile or two."""
     for V in [*range(1, 12), *range(8185, 8200), *range(16384, 16392)]:
         check_select(*make(cuda, 1, beams, V, dtype), min(4, beams * V))
+
+
+def test_parents_in_a_larger_buffer(cuda):
+    """A buffer with room for eight sequences that holds four: a fifth one is an error of the
+    caller's, not what lies there."""
+    Hq, Hkv = 4, 2
+    src, *_ = quadratic_state(cuda, 4, Hq, Hkv)
+    fp32, *_ = quadratic_state(cuda, 4, Hq, Hkv, dtype="fp32")
+    for state in (src, fp32):
+        assert state[8:12].view(torch.int32).tolist() == [4]
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device=cuda)  # noqa: E731
+    size = lambda n: oal.state_bytes(oal.make_shape(n, 1, Hq, Hkv))  # noqa: E731
+    wide = torch.full((size(8),), 0xAB, dtype=torch.uint8, device=cuda)
+    oal.state_reorder(src, i32(0, 1, 2, 3), wide, Hq, Hkv)
+    got, want = (torch.empty(size(3), dtype=torch.uint8, device=cuda) for _ in range(2))
+    oal.state_reorder(src, i32(3, 0, 2), want, Hq, Hkv)
+    oal.state_reorder(wide, i32(3, 0, 2), got, Hq, Hkv)
+    torch.cuda.synchronize()
+    assert oal.device_error() == 0 and torch.equal(got, want)
+    oal.state_reorder(wide, i32(5, -1, 2), got, Hq, Hkv)
+    assert oal.device_error() == -10 and torch.equal(got, want)
+    gen = torch.Generator().manual_seed(8)
+    q, k, v = (torch.randn(3, h, 1, 64, generator=gen).to(cuda) for h in (Hq, Hkv, Hkv))
+    ws = oal.decode_workspace(3, Hq, Hkv, cuda)
+    one = oal.decode_step_beam(q, k, v, wide, i32(4, 0, 2), got, ws)
+    assert oal.device_error() == -10
+    two = oal.decode_step(q, k, v, want, ws)
+    assert torch.equal(one, two) and torch.equal(got, want)
