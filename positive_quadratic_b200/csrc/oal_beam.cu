@@ -240,11 +240,13 @@ __device__ __forceinline__ bool better(const Candidate& a, const Candidate& b)
 
 // Block = one search.  A row is live if it has a log-softmax (a finite running score and maximum,
 // no NaN).  The candidates of the others: of an ended row the padding token at its running score;
-// everything else scores -inf.
+// everything else scores -inf.  The block may start while the scan still writes the maxima and sums:
+// these are no read-only data of this kernel (no __restrict__), or a load of them might be taken to
+// before the wait.
 template <typename T>
 __global__ void __launch_bounds__(kMergeThreads, 1) select_merge_kernel(
-    const T* __restrict__ logits, long long ld, const float* __restrict__ gmax,
-    const float* __restrict__ bmax, const Slice* __restrict__ part, int beams, int V, int n, int slices, int all_tiles,
+    const T* __restrict__ logits, long long ld, const float* gmax, const float* bmax, const Slice* part,
+    int beams, int V, int n, int slices, int all_tiles,
     const float* __restrict__ running, const uint8_t* __restrict__ ended, int pad_token,
     float* __restrict__ scores, int32_t* __restrict__ parents, int32_t* __restrict__ tokens)
 {
