@@ -638,6 +638,8 @@ def _call_on_stream(f):
         torch_c = torch._C  # (a torch without CUDA lacks the two functions)
         if stream is None and index == torch_c._cuda_getDevice():
             return f(*args, stream=torch_c._cuda_getCurrentRawStream(index), **kwargs)
+        if stream is not None and stream.device != x.device:
+            raise ValueError(f"the stream must be one of {x.device}, got one of {stream.device}")
         with _There(x.device, stream):
             return f(*args, stream=torch_c._cuda_getCurrentRawStream(index), **kwargs)
     return call

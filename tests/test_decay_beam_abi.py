@@ -388,3 +388,19 @@ else:
 """
     root = os.path.dirname(os.path.dirname(os.path.abspath(oal.__file__)))
     subprocess.run([sys.executable, "-c", code], check=True, cwd=root)
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    """The call would run on another stream than the one named."""
+    class There:  # stands for a tensor, or a stream, of a device that is not here
+        def __init__(self, index):
+            self.index, self.device = index, torch.device("cuda", index)
+
+        def get_device(self):
+            return self.index
+
+    ran = []
+    call = oal._call_on_stream(lambda x, stream: ran.append(stream))
+    with pytest.raises(ValueError, match="stream"):
+        call(There(0), stream=There(1))
+    assert not ran
