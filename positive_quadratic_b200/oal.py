@@ -891,6 +891,8 @@ def _state_of(name, t, B, Hq, Hkv, index):
     """(pointer, sequences) of a state buffer (uint8) with room for B sequences at least."""
     if t.dtype is not torch.uint8 or t.dim() != 1:
         raise TypeError(f"{name} must be a state buffer (uint8, one dimension)")
+    if Hq < 1 or Hkv < 1:
+        raise ValueError(f"Hq and Hkv must be at least 1, got {Hq} and {Hkv}")
     if t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor on cuda:{index}")
     # the layout of oal_state_bytes: header and coefficient tables, then the sequences

@@ -404,3 +404,9 @@ def test_binding_refuses_a_stream_of_another_device():
     with pytest.raises(ValueError, match="stream"):
         call(There(0), stream=There(1))
     assert not ran
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(0, 0), (2, 0), (0, 1), (-2, -1)])
+def test_state_buffers_need_heads(Hq, Hkv):
+    with pytest.raises(ValueError, match="Hq"):
+        oal._state_of("src", torch.zeros(1 << 16, dtype=torch.uint8), 1, Hq, Hkv, -1)
