@@ -103,11 +103,13 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // Block (slice, row): `tiles` tiles from slice * tiles on.  gmax [rows][all tiles][256], bmax
 // [rows][all tiles][8].  kSkew: rows need not start on 16 bytes; their vectors are put together from
-// the aligned ones that a lane and its neighbour hold.  128 rows of 50,257: a call of 15.8 us in bf16
-// and 17.6 in fp32, against 15.4 and 16.4 when rows were cut by address; 128 rows of 151,936 in bf16,
-// which start on 16 bytes: 21.4.
+// the aligned ones that a lane and its neighbour hold.  128 rows of 50,257: a call of 15.6 us in bf16
+// and 17.0 in fp32, against 15.4 and 16.6 when rows were cut by address; 128 rows of 151,936 in bf16,
+// which start on 16 bytes: 22.5, against 23.0.  (Three blocks per SM: 64 to 80 registers.  Left to
+// itself the compiler gives bf16 64 and fp32 87 where rows are skewed: with a fifth of the rows
+// ended 20.3 and 17.4 us for these two sizes, against 18.5 and 15.6.)
 template <typename T, bool kSkew>
-__global__ void __launch_bounds__(kThreads) select_scan_kernel(
+__global__ void __launch_bounds__(kThreads, 3) select_scan_kernel(
     const T* __restrict__ logits, long long ld, int rows, int V, int tiles, int all_tiles,
     const float* __restrict__ running, const uint8_t* __restrict__ ended,
     float* __restrict__ gmax, float* __restrict__ bmax, Slice* __restrict__ part)

@@ -487,6 +487,8 @@ int by_type(int dtype, F f)
 // Parts in which the heads of a group are summed (the gradient's R): enough CTAs for two per SM
 // where the chunks alone are too few, at the price of a 16 KB partial sum each.  The gradient of 4096
 // tokens of 14/2 heads: 34.9 us with two per SM, 37.0 with three; in fp32 119 us, 131 without parts.
+// (The workspace's size follows from it, so it counts the SMs of the chip the library is built for, not
+// those of the device that is current when the size is asked for.)
 constexpr int kSms = 148;
 int parts_of(const oal_shape* s, int grp)
 {
