@@ -19,9 +19,9 @@
 // and their product are off by 2.5 u of a term's exponent d = max - x, ex2 by 4 u, and a thread's sum of
 // 32 terms by 10 u.  Terms weigh e^-d, so that the mean of d is below log V <= 21.5; with the
 // same for a partial sum that moves to a larger maximum: below 128 u = 2^-17 in all.
-// The scan reads every logit once (128 rows of 151,936 in bf16, a fifth of them ended, 31 MB: 12 us,
-// 2.6 TB/s); the merge is a chain of dependent loads and barriers, 10 to 14 us whatever the size.  The
-// call takes 20.6 us there: the merge's launch is hidden behind the scan.
+// The scan reads every logit once (128 rows of 151,936 in bf16, a fifth of them ended, 31 MB: 11 us,
+// 2.8 TB/s); the merge is a chain of dependent loads and barriers, 10 to 12 us whatever the size.  The
+// call takes 20.7 us there: the merge's launch is hidden behind the scan.
 #pragma once
 
 #include <cmath>

@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 2) mix_simt_kernel(DecayShape S, Dec
 // ------------------------------------------------------------------------------------------
 // One token: block = (kv, b).  Thread (r0, c4) holds rows r0 + 16 i of the columns 4 c4 .. + 3.  The
 // state passes through registers once, all of it requested before anything is computed:
-// memory-bound, 1024 sequences of 16 heads (545 MB) in 84 us a call, 6.5 TB/s.  64 sequences of 2 heads
+// memory-bound, 1024 sequences of 16 heads (545 MB) in 84 to 86 us a call, 6.3 to 6.5 TB/s.  64 sequences of 2 heads
 // take 6 us, less than the host's call (10 us).
 // ------------------------------------------------------------------------------------------
 template <typename T>

@@ -494,7 +494,9 @@ struct MixWalk {
     }
 };
 
-// P = S o D for rows 32 qw + lane and keys 32 jb .. + 31, written over the scores.
+// P = S o D for rows 32 qw + lane and keys 32 jb .. + 31, written over the scores.  Rounded once to bf16,
+// as an operand of the next product has to be: formed and decayed in fp32, each term off by at most 2^-8
+// of itself, the sums over them in fp32 (see store_state for what it comes to).
 __device__ __forceinline__ void decay_scores(uint32_t scores, const MixInfo& I, int qw, int jb,
                                              int lane)
 {
