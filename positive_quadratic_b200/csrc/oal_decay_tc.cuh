@@ -95,17 +95,14 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_l
         : "memory");
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32])
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16])
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
         "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
-        "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
-        "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
-        "r"(v[29]), "r"(v[30]), "r"(v[31])
+        "r"(v[15])
         : "memory");
 }
 
@@ -505,10 +502,10 @@ __device__ __forceinline__ void decay_scores(uint32_t scores, const MixInfo& I, 
 {
     const int rev = I.rev;
     const int ahead = rev ? jb - qw : qw - jb;  // blocks between the rows and the keys
-    uint32_t p[32];  // what bf16 holds of P, and what it leaves
+    uint32_t p[16];
     if (ahead < 0) {
 #pragma unroll
-        for (int x = 0; x < 32; ++x) p[x] = 0u;
+        for (int x = 0; x < 16; ++x) p[x] = 0u;
     } else {
         float s[32];
         tmem_ld32(scores, s);
@@ -532,12 +529,9 @@ __device__ __forceinline__ void decay_scores(uint32_t scores, const MixInfo& I, 
             for (int x = 0; x < 32; ++x) s[x] = (live >> x) & 1 ? s[x] : 0.f;
         }
 #pragma unroll
-        for (int x = 0; x < 16; ++x) {
-            p[x] = pack_bf16x2(s[2 * x], s[2 * x + 1]);
-            p[16 + x] = pack_bf16x2(s[2 * x] - bf16lo_to_f32(p[x]), s[2 * x + 1] - bf16hi_to_f32(p[x]));
-        }
+        for (int x = 0; x < 16; ++x) p[x] = pack_bf16x2(s[2 * x], s[2 * x + 1]);
     }
-    tmem_st32(scores, p);
+    tmem_st16(scores, p);
 }
 
 __device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, int x, int y, int z)
@@ -849,9 +843,9 @@ __global__ void __launch_bounds__(kMixThreads, 2)
                 if (h > 0) mma_ts<true>(tmem + kColU, tmem + kColS, z, id_mn);
                 else mma_ts<false>(tmem + kColU, tmem + kColS, z, id_mn);
 #pragma unroll
-                for (int ks = 1; ks < 16; ++ks)  // the parts of P against 16 keys each
-                    mma_ts<true>(tmem + kColU, tmem + kColS + 32 * (ks >> 2) + 8 * (ks & 3),
-                                 z + 128 * (2 * (ks >> 2) + (ks & 1)), id_mn);
+                for (int ks = 1; ks < 8; ++ks)
+                    mma_ts<true>(tmem + kColU, tmem + kColS + 32 * (ks >> 1) + 8 * (ks & 1),
+                                 z + 128 * ks, id_mn);
                 if (h == 0 && now.has_m) {
                     const uint32_t id = now.mem_t ? id_k : id_mn, by = now.mem_t ? 2 : 128;
                     mma_ss<false>(tmem + kColF, x, m0, id);
