@@ -83,6 +83,8 @@ __device__ __forceinline__ float decay_pow(float g, int m)
 // The state before a chunk, as the mix multiplies it.  In bf16 it is rounded once, to the type of the
 // q that it meets (states that are carried or returned stay in fp32): with the scores, rounded alike,
 // an error of 0.0023 of the outputs' size where 32 bits and the rounding of the result alone make 0.0017.
+// Scores and states in two bf16 parts each make 0.0017 too, at twelve more products an item: 8 x 4096
+// tokens of 14/2 heads took 60.5 us then, 55.7 so, and the gradient of 4 x 4096 102 us, 87 so.
 __device__ __forceinline__ void store_state(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 __device__ __forceinline__ void store_state(__nv_bfloat16* p, float4 v)
 {
